@@ -322,6 +322,93 @@ int moe_layer_forward_noalloc(const moe_layer *L, const uint16_t *x_bf16, int32_
                               const moe_residual *res, int32_t *topk_ids, float *topk_w,
                               const moe_forward_opts *opts, void *stream);
 
+/* ---- Expert products on their own: 16-bit and MXFP4 weights ----
+ *
+ * The products that moe_expert_ffn makes from int8 and int4 weights, one at
+ * a time, for weights held in 16 bits (with the two gradients, for callers
+ * that train or calibrate the experts) and in MXFP4.  Rows are grouped by
+ * expert as moe_permute leaves them: rows offsets[e] .. offsets[e+1] - 1
+ * belong to expert e (int32 [E+1] on the device; NULL with E == 1: all
+ * n_rows rows).  Offsets are taken as between 0 and n_rows.  Rows of `out`
+ * outside every group are left as they were.  Groups may be empty and of
+ * any length.  E <= 1024.  Sums are held in fp32.
+ *
+ * row_tok int32 [n_rows] or NULL: row r reads row row_tok[r] of x, which
+ * has T rows; a value outside [0, T) reads a row of zeros.  NULL: row r
+ * reads row r, and n_rows <= T is required.
+ * row_w float [n_rows] or NULL: row r of the result is scaled by row_w[r].
+ * Row strides (..._ld) are in elements and at least the row's width; the
+ * elements between a row's end and the next row are not touched.  No
+ * operand may overlap the output. */
+
+typedef enum { MOE_T_BF16 = 1, MOE_T_F16 = 2, MOE_T_F32 = 3 } moe_dtype;
+
+/* MXFP4 rows (OCP Microscaling Formats v1.0: E2M1 elements, one E8M0 scale
+ * per 32 elements of a row).  A row of `cols` elements is padded with zeros
+ * to cols_p, the next multiple of 128: q holds cols_p / 2 bytes a row
+ * (element 2j in the low nibble of byte j, 2j + 1 in its high nibble), s
+ * cols_p / 32 bytes.  Both arrays are dense and 16-byte aligned.  A block's
+ * value is element * 2^(s - 127); s = 255 makes the whole block NaN. */
+typedef struct moe_mx_rows {
+  const uint8_t *q;
+  const uint8_t *s;
+} moe_mx_rows;
+
+/* Rows to MXFP4.  With amax the largest magnitude of a block, its scale is
+ * 2^(floor(log2 amax) - 2), at least 2^-127; an element is x / scale rounded
+ * to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code,
+ * magnitudes above 6 to 6), the sign kept.  A block of zeros gets scale byte
+ * 0; a block that holds a NaN or an infinity gets scale byte 255 and codes
+ * 0.  x: rows of type x_type (moe_dtype), element-aligned, stride x_ld.  q
+ * and s are written whole, the padding included.  rows = 0 is a no-op. */
+int moe_mx_quantize(const void *x, int32_t x_type, int64_t x_ld, int32_t rows, int32_t cols, uint8_t *q, uint8_t *s,
+                    void *stream);
+
+/* The values of MXFP4 rows in out_type (exact in fp32 and bf16 but for
+ * results below or above the type's range). */
+int moe_mx_dequantize(const uint8_t *q, const uint8_t *s, int32_t rows, int32_t cols, void *out, int32_t out_type,
+                      int64_t out_ld, void *stream);
+
+/* Grouped product of MXFP4 rows with MXFP4 experts.  w: rows e * N + n, K
+ * columns; x: T rows of K columns.  For row r of expert e, with
+ * p_w[n] = sum_k x[r][k] w_e[n][k]:
+ *   up NULL: out[r][n] = row_w[r] * p_w[n];
+ *   up given (same shape as w): out[r][n] = row_w[r] * silu(p_w[n]) *
+ *   p_up[n], the SwiGLU of a gate and an up matrix.
+ * Products are exact; a NaN block makes every sum it enters NaN.  out_type
+ * any moe_dtype, out element-aligned with stride out_ld.  Any N, K >= 1 up
+ * to 65536.  n_rows = 0 is a no-op. */
+int moe_mx_grouped_gemm(const moe_mx_rows *x, int32_t T, int32_t n_rows, const moe_mx_rows *w, const moe_mx_rows *up,
+                        int32_t E, int32_t N, int32_t K, const int32_t *offsets, const int32_t *row_tok,
+                        const float *row_w, void *out, int32_t out_type, int64_t out_ld, void *stream);
+
+/* Grouped product in 16 bits: out[r][n] = row_w[r] * sum_k x[r][k]
+ * w_e[n][k].  x rows and w [E][N][K] (dense) of type `type` (BF16 or F16);
+ * out_type = type or F32.  N and K multiples of 8 up to 65536; inputs
+ * 16-byte aligned with strides that are multiples of 8 elements; out
+ * 16-byte aligned, its stride a multiple of 8.  n_rows = 0 is a no-op. */
+int moe_grouped_gemm(const void *x, int64_t x_ld, int32_t T, int32_t n_rows, const void *w, int32_t type, int32_t E,
+                     int32_t N, int32_t K, const int32_t *offsets, const int32_t *row_tok, const float *row_w,
+                     void *out, int32_t out_type, int64_t out_ld, void *stream);
+
+/* Its gradient by the rows: dx[r][k] = sum_n dy[r][n] w_e[n][k], dy being
+ * the gradient by the unscaled product (row_w[r] times the gradient by out)
+ * and dx that by the gathered rows: the gradient by a token is the sum of
+ * its rows, as moe_combine forms it from float rows.  Types, sizes and
+ * alignment as moe_grouped_gemm. */
+int moe_grouped_gemm_dx(const void *dy, int64_t dy_ld, int32_t n_rows, const void *w, int32_t type, int32_t E,
+                        int32_t N, int32_t K, const int32_t *offsets, void *dx, int32_t out_type, int64_t dx_ld,
+                        void *stream);
+
+/* Its gradient by the matrices: dw[e][n][k] = sum over the rows r of expert
+ * e of dy[r][n] x[r][k] (dense [E][N][K]); an expert without rows gets
+ * zeros, also when n_rows = 0 (dy, x and row_tok may then be NULL).  The
+ * sums run over r in order of the matrix cores' blocks, the same for
+ * identical inputs. */
+int moe_grouped_gemm_dw(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, int32_t T, int32_t n_rows,
+                        int32_t type, int32_t E, int32_t N, int32_t K, const int32_t *offsets,
+                        const int32_t *row_tok, void *dw, int32_t out_type, void *stream);
+
 /* ---- Measurement helpers (not on the layer path) ----
  *
  * The achievable ceilings the expert kernels are compared with, measured on

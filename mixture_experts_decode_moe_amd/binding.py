@@ -57,7 +57,16 @@ class MoeLayer(ctypes.Structure):
                 ("routed", MoeExperts), ("shared", MoeExperts), ("shared_gate_w", ctypes.c_void_p)]
 
 
+class MoeMxRows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+
+
+MOE_T_BF16, MOE_T_F16, MOE_T_F32 = 1, 2, 3
+DTYPES = {torch.bfloat16: MOE_T_BF16, torch.float16: MOE_T_F16, torch.float32: MOE_T_F32}
+
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_i64 = ctypes.c_int64
+_PM = ctypes.POINTER(MoeMxRows)
 _PL = ctypes.POINTER(MoeLayer)
 _PE = ctypes.POINTER(MoeExperts)
 _PR = ctypes.POINTER(MoeResidual)
@@ -80,6 +89,15 @@ _SIGS = {
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "moe_calib_mfma": ([_i32, _i32, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_double), _vp],
                        ctypes.c_int),
+    "moe_mx_quantize": ([_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "moe_mx_dequantize": ([_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp], ctypes.c_int),
+    "moe_mx_grouped_gemm": ([_PM, _i32, _i32, _PM, _PM, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp],
+                            ctypes.c_int),
+    "moe_grouped_gemm": ([_vp, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp],
+                         ctypes.c_int),
+    "moe_grouped_gemm_dx": ([_vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i64, _vp], ctypes.c_int),
+    "moe_grouped_gemm_dw": ([_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp],
+                            ctypes.c_int),
     "moe_calib_read": ([_vp, _sz, ctypes.POINTER(ctypes.c_float), _vp], ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
@@ -312,6 +330,152 @@ def stack_forward(c_layers, x_bf16, residual_in, residual_out, normed_out, y, ws
     _check("moe_stack_forward", _lib.moe_stack_forward(
         c_layers, len(c_layers), _ptr(x_bf16), T, _ptr(residual_in), _ptr(residual_out), _ptr(normed_out), eps,
         _ptr(y), _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------------ grouped products, MXFP4
+
+def mx_cols(cols: int) -> int:
+    """Elements of an MXFP4 row of `cols` elements with its padding (a multiple of 128)."""
+    return -(-cols // 128) * 128
+
+
+def _rows(t, name):
+    """A matrix whose rows are contiguous (any row stride): (pointer, row stride, rows, columns, type)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    if rows <= 1:
+        ld = max(ld, cols)  # the stride of a single row says nothing
+    elif ld < cols:
+        raise ValueError(f"{name}: rows overlap")
+    kind = DTYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32")
+    return t.data_ptr(), ld, rows, cols, kind
+
+
+def _dense(t, name, dtype, n, dev):
+    """A contiguous device array of at least n values, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() < n:
+        raise ValueError(f"{name}: expected {n} values of {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on another device")
+    return _ptr(t)
+
+
+def _mx(m, name, rows, cols, dev):
+    """The C struct of MXFP4 rows (q, s)."""
+    p = mx_cols(cols)
+    q, s = m
+    return MoeMxRows(_dense(q, name + " codes", torch.uint8, rows * (p // 2), dev),
+                     _dense(s, name + " scales", torch.uint8, rows * (p // 32), dev))
+
+
+def _same_type(kind, others, what):
+    if any(k != kind for k in others):
+        raise ValueError(f"{what} have to be of one 16-bit type")
+
+
+def _call(fn, dev, stream, *args):
+    """Runs an entry point with `dev` current (its stream and launches belong to that device)."""
+    f = getattr(_lib, fn)
+    if dev.index == torch.cuda.current_device():
+        rc = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _stream(stream))
+    _check(fn, rc)
+
+
+def mx_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
+    """moe_mx_quantize: rows of x [rows][cols] (bfloat16, float16 or float32, any row stride) to codes q uint8
+    [rows][mx_cols(cols) / 2] and scales s uint8 [rows][mx_cols(cols) / 32]."""
+    xp, ld, rows, cols, kind = _rows(x, "x")
+    m = _mx((q, s), "x", rows, cols, x.device)
+    _call("moe_mx_quantize", x.device, stream, xp, kind, ld, rows, cols, m.q, m.s)
+
+
+def mx_dequantize(q: torch.Tensor, s: torch.Tensor, out: torch.Tensor, stream=None):
+    """moe_mx_dequantize: the values of MXFP4 rows into out [rows][cols]."""
+    op, ld, rows, cols, kind = _rows(out, "out")
+    m = _mx((q, s), "out", rows, cols, out.device)
+    _call("moe_mx_dequantize", out.device, stream, m.q, m.s, rows, cols, op, kind, ld)
+
+
+def mx_grouped_gemm(x, w, n_experts: int, K: int, offsets, out: torch.Tensor, up=None, row_tok=None, row_w=None,
+                    stream=None):
+    """moe_mx_grouped_gemm: out [n_rows][N] from MXFP4 pairs (codes, scales): x (T rows), w and up (n_experts * N
+    rows) of K columns each.  offsets int32 [n_experts + 1] or None (one expert)."""
+    op, ld, n_rows, N, kind = _rows(out, "out")
+    dev = out.device
+    T = x[0].numel() // (mx_cols(K) // 2)
+    xm, wm = _mx(x, "x", T, K, dev), _mx(w, "w", n_experts * N, K, dev)
+    um = None if up is None else _mx(up, "up", n_experts * N, K, dev)
+    _call("moe_mx_grouped_gemm", dev, stream, ctypes.byref(xm), T, n_rows, ctypes.byref(wm),
+          None if um is None else ctypes.byref(um), n_experts, N, K,
+          _dense(offsets, "offsets", torch.int32, n_experts + 1, dev),
+          _dense(row_tok, "row_tok", torch.int32, n_rows, dev), _dense(row_w, "row_w", torch.float32, n_rows, dev),
+          op, kind, ld)
+
+
+def _weights(w, name, dev):
+    """[E][N][K] contiguous matrices: (pointer, E, N, K, type)."""
+    if w.dim() != 3 or w.device != dev:
+        raise ValueError(f"{name}: expected [E][N][K] on the rows' device")
+    kind = DTYPES.get(w.dtype)
+    if kind is None:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32")
+    return (_ptr(w), *w.shape, kind)
+
+
+def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets, out: torch.Tensor, row_tok=None, row_w=None, stream=None):
+    """moe_grouped_gemm: out [n_rows][N] from rows x [T][K] and matrices w [E][N][K] of one 16-bit type; out of that
+    type or float32."""
+    xp, x_ld, T, K, kind = _rows(x, "x")
+    dev = x.device
+    wp, E, N, wk, wkind = _weights(w, "w", dev)
+    op, out_ld, n_rows, on, okind = _rows(out, "out")
+    _same_type(kind, (wkind,), "x and w")
+    if wk != K or on != N or out.device != dev:
+        raise ValueError("x [T][K], w [E][N][K] and out [n_rows][N] do not fit")
+    _call("moe_grouped_gemm", dev, stream, xp, x_ld, T, n_rows, wp, kind, E, N, K,
+          _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),
+          _dense(row_w, "row_w", torch.float32, n_rows, dev), op, okind, out_ld)
+
+
+def grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, offsets, dx: torch.Tensor, stream=None):
+    """moe_grouped_gemm_dx: dx [n_rows][K] from dy [n_rows][N] and w [E][N][K]."""
+    yp, y_ld, n_rows, N, kind = _rows(dy, "dy")
+    dev = dy.device
+    wp, E, wn, K, wkind = _weights(w, "w", dev)
+    op, out_ld, rows, ok, okind = _rows(dx, "dx")
+    _same_type(kind, (wkind,), "dy and w")
+    if wn != N or ok != K or rows != n_rows or dx.device != dev:
+        raise ValueError("dy [n_rows][N], w [E][N][K] and dx [n_rows][K] do not fit")
+    _call("moe_grouped_gemm_dx", dev, stream, yp, y_ld, n_rows, wp, kind, E, N, K,
+          _dense(offsets, "offsets", torch.int32, E + 1, dev), op, okind, out_ld)
+
+
+def grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, offsets, dw: torch.Tensor, row_tok=None, stream=None):
+    """moe_grouped_gemm_dw: dw [E][N][K] from dy [n_rows][N] and rows x [T][K]."""
+    yp, y_ld, n_rows, N, kind = _rows(dy, "dy")
+    dev = dy.device
+    xp, x_ld, T, K, xkind = _rows(x, "x")
+    op, E, on, ok, okind = _weights(dw, "dw", dev)
+    _same_type(kind, (xkind,), "dy and x")
+    if on != N or ok != K or x.device != dev:
+        raise ValueError("dy [n_rows][N], x [T][K] and dw [E][N][K] do not fit")
+    _call("moe_grouped_gemm_dw", dev, stream, yp, y_ld, xp, x_ld, T, n_rows, kind, E, N, K,
+          _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),
+          op, okind)
 
 
 def calib_mfma(kind: int, iters: int, stream=None):

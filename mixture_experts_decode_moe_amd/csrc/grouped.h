@@ -1,0 +1,64 @@
+// Arguments of the grouped products and of the MXFP4 conversions, shared by
+// their host side and kernels.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+constexpr int kMxBlock = 32;  // elements under one scale
+constexpr int kMxPad = 128;   // rows are padded to a multiple of this
+
+struct MxQuantArgs {
+  const void *x;
+  int64_t x_ld;
+  int32_t rows, cols, type;
+  uint8_t *q, *s;
+};
+hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t s);
+
+struct MxDequantArgs {
+  const uint8_t *q, *s;
+  int32_t rows, cols, type;
+  void *out;
+  int64_t out_ld;
+};
+hipError_t launch_mx_dequantize(const MxDequantArgs &a, hipStream_t s);
+
+// One grouped product.  The output tile is [b][a]: `a` is the operand whose
+// rows become the contiguous output columns (the matrices; for dw: x), `b`
+// the one whose rows become output rows (the grouped rows; for dw: dy).
+enum GroupedKind : int32_t { kGroupedFwd, kGroupedDx, kGroupedDw, kGroupedMx };
+
+struct GroupedArgs {
+  int32_t kind, type, out_type;
+  const char *a, *a2;    // matrices (and SwiGLU's up matrices); dw: x
+  const char *b;         // rows; dw: dy
+  const char *as, *as2, *bs;  // MXFP4 scales
+  int64_t a_ld, b_ld;    // bytes a row
+  int64_t a_expert;      // bytes a matrix (0 for dw)
+  int32_t s_ld;          // MXFP4: scale bytes a row
+  int32_t T, n_rows, E;
+  int32_t na;            // output columns
+  int32_t nb;            // dw: output rows (N)
+  int32_t red;           // length of the reduction: bytes of a row (fwd, mx) or rows (dx); dw: per group
+  const int32_t *offsets, *row_tok;
+  const float *row_w;
+  char *out;
+  int64_t out_ld;        // elements
+  int32_t out_vec;       // out rows are 16-byte aligned
+};
+hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s);
+
+// Rows of group e, inside [0, n_rows) whatever the offsets hold.
+struct GroupRange {
+  int r0, n;
+};
+MOE_DEV GroupRange group_range(const GroupedArgs &a, int e) {
+  if (!a.offsets) return GroupRange{0, a.n_rows};
+  const int lo = min(max(a.offsets[e], 0), a.n_rows);
+  const int hi = min(max(a.offsets[e + 1], lo), a.n_rows);
+  return GroupRange{lo, hi - lo};
+}
+
+}  // namespace moe

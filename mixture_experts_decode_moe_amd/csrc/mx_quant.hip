@@ -1,0 +1,213 @@
+// Rows to MXFP4 and back (moe_mx_quantize, moe_mx_dequantize).
+//
+// A block of 32 elements has one scale 2^e with e = floor(log2 amax) - 2, so
+// that its largest magnitude lands in [4, 8), the top binade of the E2M1
+// grid {0, 0.5, 1, 1.5, 2, 3, 4, 6}.  The exponent field of amax is
+// floor(log2 amax) + 127 for every normal float, and anything smaller takes
+// the smallest scale, 2^-127, so the scale byte is max(field - 2, 0): no
+// logarithm and no rounding.  Dividing by a power of two is exact, so
+// v_cvt_scalef32_pk_fp4_f32 rounds once, to the nearest code, ties to even,
+// clamped at 6; it agrees with the integer definition at all borders, down
+// to 2^-127.
+//
+// Both kernels do a handful of operations a byte and are bound by HBM.  A
+// row's 128 elements (the padding unit) belong to 16 lanes of eight elements:
+// a lane's 16-bit input is one 16-byte load, its codes one 4-byte word, four
+// lanes share a block, and one lane in 16 writes the unit's four scale bytes
+// as a word.
+#include "grouped.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMxThreads = 256;
+constexpr int kMxUnits = kMxThreads / 16;  // 128-element units a block works on at a time
+constexpr int kMxMaxBlocks = 256 * 16;
+
+// Unit u, u + stride, ... of a row-major array of `upr` units a row, without
+// a division a step.
+struct UnitWalk {
+  int64_t row;
+  int32_t unit, drow, dunit, upr;
+  MOE_DEV UnitWalk(int64_t first, int64_t stride, int32_t upr_) : upr(upr_) {
+    row = first / upr;
+    unit = static_cast<int32_t>(first - row * upr);
+    drow = static_cast<int32_t>(stride / upr);
+    dunit = static_cast<int32_t>(stride - static_cast<int64_t>(drow) * upr);
+  }
+  MOE_DEV void next() {
+    row += drow;
+    unit += dunit;
+    if (unit >= upr) {
+      unit -= upr;
+      ++row;
+    }
+  }
+};
+
+template <int TYPE>
+struct Elem;
+template <>
+struct Elem<MOE_T_BF16> {
+  using T = uint16_t;
+  static MOE_DEV float get(T v) { return bf16_to_f32(v); }
+  static MOE_DEV T put(float v) { return f32_to_bf16_rne(v); }
+};
+template <>
+struct Elem<MOE_T_F16> {
+  using T = uint16_t;
+  static MOE_DEV float get(T v) { return f16_bits_to_f32(v); }
+  static MOE_DEV T put(float v) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)); }
+};
+template <>
+struct Elem<MOE_T_F32> {
+  using T = float;
+  static MOE_DEV float get(T v) { return v; }
+  static MOE_DEV T put(float v) { return v; }
+};
+
+// Eight elements from column c of a row; VEC: the row is whole 16-byte pieces
+// there.  Columns past the end are zeros.
+template <int TYPE, bool VEC>
+MOE_DEV void load8(const typename Elem<TYPE>::T *row, int c, int cols, float (&v)[8]) {
+  using E = Elem<TYPE>;
+  if constexpr (VEC) {
+    if (c < cols) {
+      typename E::T t[8];
+      constexpr int kPieces = sizeof(t) / 16;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        reinterpret_cast<uint4 *>(t)[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = E::get(t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? E::get(row[c + i]) : 0.f;
+  }
+}
+
+MOE_DEV uint32_t dpp_u32_xor1(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, true);
+}
+MOE_DEV uint32_t dpp_u32_xor2(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, true);
+}
+
+template <int TYPE, bool VEC>
+__global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(MxQuantArgs a, int32_t upr, int64_t units) {
+  using E = Elem<TYPE>;
+  const int lane16 = threadIdx.x & 15;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kMxUnits + (threadIdx.x >> 4);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kMxUnits;
+  UnitWalk w(first, stride, upr);
+  for (int64_t u = first; u < units; u += stride, w.next()) {
+    float v[8];
+    load8<TYPE, VEC>(static_cast<const typename E::T *>(a.x) + w.row * a.x_ld, w.unit * kMxPad + lane16 * 8, a.cols, v);
+    // magnitudes compare as their bits; infinities and NaN are above all others
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, dpp_u32_xor1(m));
+    m = max(m, dpp_u32_xor2(m));
+    const bool finite = m < 0x7F800000u;
+    const uint32_t code = finite ? static_cast<uint32_t>(max(static_cast<int>(m >> 23) - 2, 0)) : 255u;
+    const float scale = __uint_as_float(code == 0 ? 0x00400000u : code << 23);  // 2^(code - 127)
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], scale, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], scale, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], scale, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], scale, 3);
+    const size_t at = static_cast<size_t>(w.row) * upr + w.unit;  // 128-element unit
+    reinterpret_cast<uint32_t *>(a.q)[at * 16 + lane16] = finite ? q : 0u;
+    uint32_t s4 = code << (8 * (lane16 >> 2));  // the unit's four scale bytes: lanes 0, 4, 8, 12
+    s4 |= __shfl_xor(s4, 4);
+    s4 |= __shfl_xor(s4, 8);
+    if (lane16 == 0) reinterpret_cast<uint32_t *>(a.s)[at] = s4;
+  }
+}
+
+template <int TYPE, bool VEC>
+__global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(MxDequantArgs a, int32_t upr, int64_t units) {
+  using E = Elem<TYPE>;
+  const int lane16 = threadIdx.x & 15;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kMxUnits + (threadIdx.x >> 4);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kMxUnits;
+  UnitWalk w(first, stride, upr);
+  for (int64_t u = first; u < units; u += stride, w.next()) {
+    const size_t at = static_cast<size_t>(w.row) * upr + w.unit;
+    const uint32_t q = reinterpret_cast<const uint32_t *>(a.q)[at * 16 + lane16];
+    const uint32_t code = a.s[at * 4 + (lane16 >> 2)];
+    const float scale = __uint_as_float(code == 255u ? 0x7FC00000u : code == 0 ? 0x00400000u : code << 23);
+    f32x2_t p[4];
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+    typename E::T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = E::put(p[i >> 1][i & 1] * scale);
+    typename E::T *row = static_cast<typename E::T *>(a.out) + w.row * a.out_ld;
+    const int c = w.unit * kMxPad + lane16 * 8;
+    if constexpr (VEC) {
+      if (c < a.cols) {
+        constexpr int kPieces = sizeof(t) / 16;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          reinterpret_cast<uint4 *>(row + c)[i] = reinterpret_cast<const uint4 *>(t)[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < a.cols) row[c + i] = t[i];
+    }
+  }
+}
+
+// whole eight-element pieces everywhere: 16-byte requests
+bool vec_ok(const void *p, int64_t ld, int32_t cols, int32_t type) {
+  const int64_t size = type == MOE_T_F32 ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * size) % 16 == 0 && cols % 8 == 0;
+}
+
+template <class Args, class K>
+hipError_t launch_units(const Args &a, K vec, K scalar, bool use_vec, hipStream_t s) {
+  const int32_t upr = (a.cols + kMxPad - 1) / kMxPad;
+  const int64_t units = static_cast<int64_t>(a.rows) * upr;
+  const int64_t blocks = (units + kMxUnits - 1) / kMxUnits;
+  const dim3 grid(static_cast<uint32_t>(blocks < kMxMaxBlocks ? blocks : kMxMaxBlocks));
+  (use_vec ? vec : scalar)<<<grid, kMxThreads, 0, s>>>(a, upr, units);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t s) {
+  const bool v = vec_ok(a.x, a.x_ld, a.cols, a.type);
+  switch (a.type) {
+    case MOE_T_BF16:
+      return launch_units(a, mx_quantize_kernel<MOE_T_BF16, true>, mx_quantize_kernel<MOE_T_BF16, false>, v, s);
+    case MOE_T_F16:
+      return launch_units(a, mx_quantize_kernel<MOE_T_F16, true>, mx_quantize_kernel<MOE_T_F16, false>, v, s);
+    default:
+      return launch_units(a, mx_quantize_kernel<MOE_T_F32, true>, mx_quantize_kernel<MOE_T_F32, false>, v, s);
+  }
+}
+
+hipError_t launch_mx_dequantize(const MxDequantArgs &a, hipStream_t s) {
+  const bool v = vec_ok(a.out, a.out_ld, a.cols, a.type);
+  switch (a.type) {
+    case MOE_T_BF16:
+      return launch_units(a, mx_dequantize_kernel<MOE_T_BF16, true>, mx_dequantize_kernel<MOE_T_BF16, false>, v, s);
+    case MOE_T_F16:
+      return launch_units(a, mx_dequantize_kernel<MOE_T_F16, true>, mx_dequantize_kernel<MOE_T_F16, false>, v, s);
+    default:
+      return launch_units(a, mx_dequantize_kernel<MOE_T_F32, true>, mx_dequantize_kernel<MOE_T_F32, false>, v, s);
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,454 @@
+"""GPU: MXFP4 conversions bit for bit, grouped products (16-bit with both gradients, MXFP4) against 64-bit sums within
+derived bounds, at the sizes, strides, groups and values where they can go wrong."""
+import pytest
+import torch
+
+import grouped_util as gu
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def say(msg):
+    print(f"[gpu] {msg}", flush=True)
+
+
+@pytest.fixture(scope="module")
+def mb():
+    from mixture_experts_decode_moe_amd import binding
+    return binding
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def strided(t, pad, fill):
+    """t on the GPU with `pad` more elements a row, all of them `fill`."""
+    base = torch.full((t.shape[0], t.shape[1] + pad), fill, dtype=t.dtype, device="cuda")
+    base[:, :t.shape[1]] = t
+    return base[:, :t.shape[1]]
+
+
+# ---- MXFP4 ------------------------------------------------------------------
+
+def encode(mb, x, **kw):
+    rows, cols = x.shape
+    q = torch.full((rows, gu.padded(cols) // 2), 0xAB, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, gu.padded(cols) // 32), 0xCD, dtype=torch.uint8, device="cuda")
+    mb.mx_quantize(x, q, s, **kw)
+    return q, s
+
+
+def same_codes(got, want):
+    assert torch.equal(got[1].cpu(), want[1])
+    assert torch.equal(got[0].cpu(), want[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 31, 0), (5, 33, 3), (7, 128, 0), (17, 200, 8), (130, 2048, 0),
+                                           (9, 1000, 24), (4100, 129, 0)])
+def test_mx_quantize_bits(mb, dtype, rows, cols, pad):
+    g = torch.Generator().manual_seed(rows * 1000 + cols)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(2 * torch.randn(rows, 1, generator=g))
+    x = x.clamp(-6e4, 6e4).to(dtype)
+    say(f"quantise {dtype} {rows}x{cols} pad {pad}")
+    xd = strided(x, pad, float("nan"))
+    got = encode(mb, xd)
+    same_codes(got, gu.mx_encode(x.float()))
+    for out_dtype in (F32, BF, HF):
+        out = strided(torch.zeros(rows, cols, dtype=out_dtype), pad, 7.0)
+        mb.mx_dequantize(*got, out)
+        want = gu.mx_decode(got[0].cpu(), got[1].cpu(), cols).to(out_dtype)
+        assert torch.equal(out.cpu(), want)
+        if pad:  # between the rows nothing is written
+            assert bool((out.as_strided((rows, pad), (cols + pad, 1), cols) == 7.0).all())
+
+
+def test_mx_quantize_every_16_bit_value(mb):
+    """Every finite bfloat16 and float16 value as a block's largest and beside larger ones, and the borders of the grid
+    at both ends of fp32's range."""
+    say("quantise: all 16-bit values")
+    for dtype in (BF, HF):
+        v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype)
+        v = v[torch.isfinite(v)]
+        x = torch.zeros(v.numel(), 64, dtype=dtype)
+        x[:, 0] = v
+        x[:, 32] = v
+        x[:, 40] = torch.roll(v, 1)
+        x[:, 63] = torch.roll(v, 77)
+        same_codes(encode(mb, x.cuda()), gu.mx_encode(x.float()))
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0])
+    around = torch.cat([border, torch.nextafter(border, torch.zeros(9)), torch.nextafter(border, torch.full((9,), 9.0))])
+    x = torch.zeros(250, 32)
+    for i, e in enumerate(range(-126, 124)):
+        x[i, :27] = torch.ldexp(around * torch.where(torch.arange(27) % 2 == 0, 1.0, -1.0), torch.tensor(e))
+        x[i, 27] = torch.ldexp(torch.tensor(4.5), torch.tensor(e))
+    same_codes(encode(mb, x.cuda()), gu.mx_encode(x))
+
+
+def test_mx_quantize_non_finite_denormal_and_zero_blocks(mb):
+    x = torch.randn(6, 160, generator=torch.Generator().manual_seed(1))
+    x[0, 3] = float("inf")
+    x[1, 40] = float("-inf")
+    x[2, 159] = float("nan")
+    x[3] = 0
+    x[4, 5:9] = -0.0
+    x[5] = torch.randint(-9, 9, (160,), generator=torch.Generator().manual_seed(2)) * 2.0 ** -149  # fp32's smallest steps
+    say("quantise: non-finite, denormal, zero")
+    got = encode(mb, x.cuda())
+    same_codes(got, gu.mx_encode(x))
+    out = torch.empty(6, 160, device="cuda")
+    mb.mx_dequantize(*got, out)
+    assert torch.equal(out.cpu().isnan(), gu.mx_decode(*gu.mx_encode(x), 160).isnan())
+
+
+# ---- grouped products -----------------------------------------------------------
+
+def cases():
+    """(label, E, offsets or None, n_rows): groups of length zero and one, beside and across tile borders, one large
+    group among empty ones, rows before the first group and behind the last, more experts than rows."""
+    def off(counts, first=0):
+        return torch.tensor([first] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+
+    g = torch.Generator().manual_seed(5)
+    many = torch.zeros(1024, dtype=torch.int64)
+    many[torch.randperm(1024, generator=g)[:40]] = 1
+    many[1023] = 3
+    return [
+        ("one expert, one row", 1, None, 1),
+        ("one expert, no offsets", 1, None, 200),
+        ("no rows in any group", 3, off([0, 0, 0]), 5),
+        ("ragged", 7, off([130, 0, 127, 1, 64, 16, 300]), 638),
+        ("rows outside the groups", 5, off([17, 0, 33, 2, 15], first=6), 90),
+        ("decode", 64, off(torch.bincount(torch.randint(0, 64, (40,), generator=g), minlength=64).tolist()), 40),
+        ("1024 experts", 1024, off(many.tolist()), int(many.sum())),
+    ]
+
+
+CASES = {c[0]: c for c in cases()}
+
+
+def tokens(n_rows, T, seed):
+    """Source rows with repeats and some out of range (they read zeros)."""
+    t = torch.randint(0, T, (n_rows,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32)
+    if n_rows > 8:
+        t[1], t[5], t[7] = -1, T, t[6]
+    return t
+
+
+def check(out, ref, mag, used, dtype, length, step, label):
+    """Rows in groups within the bound, the others as they were (7)."""
+    got = out.cpu().double()
+    assert bool((got[~used] == 7.0).all()), "rows outside the groups were written"
+    limit = gu.rounded(ref, gu.sum_bound(mag, length, step), dtype)
+    diff = (got - ref).abs()[used]
+    worst = float((diff / limit[used]).max()) if diff.numel() else 0.0
+    say(f"  {label}: at most {worst:.2f} of the bound")
+    assert bool((diff <= limit[used]).all())
+
+
+@pytest.mark.parametrize("label", list(CASES))
+@pytest.mark.parametrize("N,K,dtype,out_dtype", [(8, 8, BF, F32), (136, 72, HF, HF), (264, 1000, BF, BF)])
+def test_grouped_gemm(mb, label, N, K, dtype, out_dtype):
+    _, E, offsets, n_rows = CASES[label]
+    g = torch.Generator().manual_seed(N + n_rows)
+    for gather in (False, True):
+        say(f"grouped_gemm {label} N={N} K={K} {dtype} gather={gather}")
+        T = n_rows if not gather else max(1, n_rows // 3)
+        x = torch.randn(T, K, generator=g).to(dtype)
+        w = (torch.randn(E, N, K, generator=g) / K ** 0.5).to(dtype)
+        tok = tokens(n_rows, T, 3) if gather else None
+        row_w = torch.rand(n_rows, generator=g) if gather else None
+        out = strided(torch.full((n_rows, N), 7.0, dtype=out_dtype), 8, 7.0)
+        mb.grouped_gemm(strided(x, 16, float("nan")), dev(w), dev(offsets), out, row_tok=dev(tok), row_w=dev(row_w))
+        y, m = gu.product(gu.gathered(x, tok, n_rows), w.double(), offsets, n_rows)
+        if row_w is not None:
+            y, m = y * row_w[:, None].double(), m * row_w[:, None].double() * (1 + 2.0 ** -10)
+        check(out, y, m, gu.in_groups(offsets, n_rows), out_dtype, K, 32, label)
+
+
+@pytest.mark.parametrize("label", list(CASES))
+@pytest.mark.parametrize("N,K,dtype,out_dtype", [(8, 8, HF, F32), (72, 136, BF, BF), (1000, 264, HF, HF)])
+def test_grouped_gemm_dx(mb, label, N, K, dtype, out_dtype):
+    _, E, offsets, n_rows = CASES[label]
+    say(f"grouped_gemm_dx {label} N={N} K={K} {dtype}")
+    g = torch.Generator().manual_seed(N + n_rows)
+    dy = torch.randn(n_rows, N, generator=g).to(dtype)
+    w = (torch.randn(E, N, K, generator=g) / N ** 0.5).to(dtype)
+    out = strided(torch.full((n_rows, K), 7.0, dtype=out_dtype), 8, 7.0)
+    mb.grouped_gemm_dx(strided(dy, 8, float("nan")), dev(w), dev(offsets), out)
+    y, m = gu.product(dy.double(), w.double().transpose(1, 2).contiguous(), offsets, n_rows)
+    check(out, y, m, gu.in_groups(offsets, n_rows), out_dtype, N, 32, label)
+
+
+@pytest.mark.parametrize("label", list(CASES))
+@pytest.mark.parametrize("N,K,dtype,out_dtype", [(8, 8, BF, BF), (136, 200, HF, F32)])
+def test_grouped_gemm_dw(mb, label, N, K, dtype, out_dtype):
+    _, E, offsets, n_rows = CASES[label]
+    g = torch.Generator().manual_seed(N + n_rows)
+    used = gu.in_groups(offsets, n_rows)
+    for gather in (False, True):
+        say(f"grouped_gemm_dw {label} N={N} K={K} {dtype} gather={gather}")
+        T = n_rows if not gather else max(1, n_rows // 3)
+        x = torch.randn(T, K, generator=g).to(dtype)
+        dy = torch.randn(n_rows, N, generator=g).to(dtype)
+        tok = tokens(n_rows, T, 4) if gather else None
+        rows = gu.gathered(x, tok, n_rows)
+        ref = torch.zeros(E, N, K, dtype=torch.float64)
+        mag = torch.zeros_like(ref)
+        most = 0
+        for e, a, b in gu.groups(offsets, n_rows, E):
+            ref[e] = dy[a:b].double().T @ rows[a:b]
+            mag[e] = dy[a:b].double().abs().T @ rows[a:b].abs()
+            most = max(most, b - a)
+        dy = dy.clone()
+        dy[~used] = float("nan")  # rows of no group reach no sum
+        out = torch.full((E, N, K), 7.0, dtype=out_dtype, device="cuda")
+        mb.grouped_gemm_dw(strided(dy, 8, float("nan")), strided(x, 8, float("nan")), dev(offsets), out, row_tok=dev(tok))
+        limit = gu.rounded(ref, gu.sum_bound(mag, max(1, most), 32), out_dtype)
+        diff = (out.cpu().double() - ref).abs()
+        assert bool((diff <= limit).all())
+
+
+def test_grouped_gemm_dw_without_rows_is_zero(mb):
+    say("dw, n_rows = 0")
+    out = torch.full((3, 16, 24), 7.0, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    mb.grouped_gemm_dw(torch.empty(0, 16, dtype=BF, device="cuda"), torch.ones(5, 24, dtype=BF, device="cuda"), off, out)
+    assert not bool(out.any())
+
+
+@pytest.mark.parametrize("label", list(CASES))
+@pytest.mark.parametrize("N,K,swiglu,out_dtype", [(1, 1, False, F32), (7, 33, True, BF), (130, 200, False, HF),
+                                                  (129, 520, True, F32), (256, 512, False, BF)])
+def test_mx_grouped_gemm(mb, label, N, K, swiglu, out_dtype):
+    _, E, offsets, n_rows = CASES[label]
+    if E == 1024:
+        N = min(N, 40)
+    g = torch.Generator().manual_seed(N + n_rows + K)
+    for gather in (False, True):
+        say(f"mx_grouped_gemm {label} N={N} K={K} swiglu={swiglu} gather={gather}")
+        T = n_rows if not gather else max(1, n_rows // 3)
+
+        def codes(rows, scale):
+            return gu.mx_encode(torch.randn(rows, K, generator=g) * scale * torch.exp(torch.randn(rows, 1, generator=g)))
+
+        x, w, up = codes(T, 1.0), codes(E * N, K ** -0.5), codes(E * N, K ** -0.5) if swiglu else None
+        tok = tokens(n_rows, T, 5) if gather else None
+        row_w = torch.rand(n_rows, generator=g) if gather else None
+        out = strided(torch.full((n_rows, N), 7.0, dtype=out_dtype), 5 if N % 2 else 8, 7.0)
+        mb.mx_grouped_gemm((dev(x[0]), dev(x[1])), (dev(w[0]), dev(w[1])), E, K, dev(offsets), out,
+                           up=None if up is None else (dev(up[0]), dev(up[1])), row_tok=dev(tok), row_w=dev(row_w))
+        rows = gu.gathered(gu.mx_decode(*x, K), tok, n_rows)
+        y, m = gu.product(rows, gu.mx_decode(*w, K).reshape(E, N, K), offsets, n_rows)
+        m = gu.sum_bound(m, K, 128)
+        if swiglu:
+            u, mu = gu.product(rows, gu.mx_decode(*up, K).reshape(E, N, K), offsets, n_rows)
+            mu = gu.sum_bound(mu, K, 128)
+            # |silu'| <= 1.1; the exponential, the quotient and the products round a few times (2^-20 in all)
+            a = gu.silu(y)
+            m = 1.1 * m * (u.abs() + mu) + (a.abs() + 1.1 * m) * mu + 2.0 ** -20 * (a * u).abs()
+            y = a * u
+        if row_w is not None:
+            y, m = y * row_w[:, None].double(), (m + 2.0 ** -23 * y.abs()) * row_w[:, None].double()
+        got = out.cpu().double()
+        used = gu.in_groups(offsets, n_rows)
+        assert bool((got[~used] == 7.0).all())
+        limit = gu.rounded(y, m, out_dtype)
+        assert bool(((got - y).abs()[used] <= limit[used]).all())
+        pad = out.as_strided((n_rows, 5 if N % 2 else 8), (out.stride(0), 1), N)
+        assert bool((pad == 7.0).all())
+
+
+def test_mx_nan_blocks_reach_only_their_sums(mb):
+    """A NaN block of one row makes that row NaN, one of a weight row that column; infinities in 16 bits likewise."""
+    say("NaN blocks")
+    g = torch.Generator().manual_seed(9)
+    x, w = torch.randn(40, 200, generator=g), torch.randn(70, 200, generator=g)
+    x[3, 150] = float("inf")
+    w[66, 10] = float("nan")
+    out = torch.empty(40, 70, device="cuda")
+    mb.mx_grouped_gemm(tuple(map(dev, gu.mx_encode(x))), tuple(map(dev, gu.mx_encode(w))), 1, 200, None, out)
+    want = torch.zeros(40, 70, dtype=torch.bool)
+    want[3], want[:, 66] = True, True
+    assert torch.equal(out.isnan().cpu(), want)
+
+
+def test_offsets_outside_the_rows_are_clamped(mb):
+    """Offsets below zero, above n_rows or falling leave memory alone: groups are cut to the rows there are."""
+    say("bad offsets")
+    x = torch.randn(20, 64, generator=torch.Generator().manual_seed(2)).to(BF)
+    w = torch.randn(4, 16, 64, generator=torch.Generator().manual_seed(3)).to(BF)
+    off = torch.tensor([-7, 5, 3, 12, 4000], dtype=torch.int32)
+    out = torch.full((24, 16), 7.0, device="cuda")
+    mb.grouped_gemm(dev(x), dev(w), dev(off), out[:20])
+    want = torch.tensor([0, 5, 5, 12, 20], dtype=torch.int32)  # rows 3..4 belong to experts 0 and 2
+    y, m = gu.product(x.double(), w.double(), want, 20)
+    sure = torch.ones(20, dtype=torch.bool)
+    sure[3:5] = False
+    diff = (out[:20].cpu().double() - y).abs()[sure]
+    assert bool((diff <= gu.rounded(y, gu.sum_bound(m, 64, 32), F32)[sure]).all())
+    assert bool((out[20:] == 7.0).all())
+
+
+# ---- as they are used -----------------------------------------------------------
+
+def route(mb, T, E, topk, seed):
+    """A permutation by expert from moe_permute."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.stack([torch.randperm(E, generator=g)[:topk] for _ in range(T)]).to(torch.int32).cuda()
+    wts = torch.rand(T, topk, generator=g).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = {"counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32), "row_tok": torch.empty(T * topk, **i32),
+           "row_w": torch.empty(T * topk, device="cuda"), "inv_pos": torch.empty(T, topk, **i32),
+           "active": torch.empty(E, **i32), "n_active": torch.empty(1, **i32)}
+    ws = torch.empty(mb.permute_workspace_bytes(T, topk, E), dtype=torch.uint8, device="cuda")
+    mb.permute(ids, wts, E, out, ws)
+    return out
+
+
+class MxLayer:
+    """The routed experts on MXFP4: tokens quantised once, gate/up with SwiGLU, quantised again, down, combined."""
+
+    def __init__(self, mb, T, E, topk, H, F, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.mb, self.T, self.E, self.topk, self.H, self.F = mb, T, E, topk, H, F
+        self.p = route(mb, T, E, topk, seed)
+        self.x = torch.randn(T, H, generator=g).to(BF).cuda()
+        self.w = {n: (torch.randn(E, r, c, generator=g) / c ** 0.5) for n, r, c in
+                  (("gate", F, H), ("up", F, H), ("down", H, F))}
+        self.q = {n: encode(mb, w.reshape(-1, w.shape[2]).cuda()) for n, w in self.w.items()}
+        rows = T * topk
+        u8 = dict(dtype=torch.uint8, device="cuda")
+        self.xq = (torch.empty(T, gu.padded(H) // 2, **u8), torch.empty(T, gu.padded(H) // 32, **u8))
+        self.aq = (torch.empty(rows, gu.padded(F) // 2, **u8), torch.empty(rows, gu.padded(F) // 32, **u8))
+        self.act = torch.empty(rows, F, dtype=BF, device="cuda")
+        self.rows = torch.empty(rows, H, device="cuda")
+        self.y = torch.empty(T, H, device="cuda")
+
+    def run(self, stream=None):
+        mb, p = self.mb, self.p
+        mb.mx_quantize(self.x, *self.xq, stream=stream)
+        mb.mx_grouped_gemm(self.xq, self.q["gate"], self.E, self.H, p["offsets"], self.act, up=self.q["up"],
+                           row_tok=p["row_tok"], stream=stream)
+        mb.mx_quantize(self.act, *self.aq, stream=stream)
+        mb.mx_grouped_gemm(self.aq, self.q["down"], self.E, self.F, p["offsets"], self.rows, row_w=p["row_w"], stream=stream)
+        mb.combine(self.rows, p["inv_pos"], self.T, self.topk, self.H, None, self.y, stream=stream)
+        return self.y
+
+
+@pytest.mark.parametrize("T", [1, 16, 300])
+def test_mx_layer(mb, T):
+    """Each stage of the run against 64 bits on the stage's own inputs."""
+    say(f"MXFP4 layer T={T}")
+    L = MxLayer(mb, T, 32, 4, 512, 256, 40 + T)
+    y = L.run().cpu().double()
+    off, tok = L.p["offsets"].cpu(), L.p["row_tok"].cpu()
+    n = T * 4
+    same_codes(L.xq, gu.mx_encode(L.x.cpu().float()))
+    same_codes(L.aq, gu.mx_encode(L.act.cpu().float()))
+    dec = {k: gu.mx_decode(v[0].cpu(), v[1].cpu(), L.w[k].shape[2]).reshape(L.w[k].shape) for k, v in L.q.items()}
+    xr = gu.gathered(gu.mx_decode(L.xq[0].cpu(), L.xq[1].cpu(), 512), tok, n)
+    a, _ = gu.product(xr, dec["gate"], off, n)
+    u, _ = gu.product(xr, dec["up"], off, n)
+    act = gu.silu(a) * u
+    assert float((L.act.cpu().double() - act).norm() / act.norm()) < 2.0 ** -8
+    ar = gu.mx_decode(L.aq[0].cpu(), L.aq[1].cpu(), 256)
+    d, m = gu.product(ar, dec["down"], off, n)
+    rw = L.p["row_w"].cpu().double()[:, None]
+    d, m = d * rw, (gu.sum_bound(m, 256, 128) + 2.0 ** -23 * d.abs()) * rw
+    assert bool(((L.rows.cpu().double() - d).abs() <= gu.rounded(d, m, F32)).all())
+    inv = L.p["inv_pos"].cpu().long()
+    ref = L.rows.cpu().double()[inv].sum(1)
+    assert bool(((y - ref).abs() <= 4 * 2.0 ** -24 * L.rows.cpu().double()[inv].abs().sum(1)).all())
+
+
+def test_mx_layer_captured_and_on_another_stream(mb):
+    """A captured run replayed between eager ones, and a run on a side stream, give the eager bits."""
+    say("MXFP4 layer: graph and streams")
+    L = MxLayer(mb, 24, 32, 4, 512, 256, 77)
+    eager = L.run().clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    L.y.zero_()
+    torch.cuda.synchronize()
+    L.run(stream=side)
+    side.synchronize()
+    assert torch.equal(L.y, eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.run()
+    other = MxLayer(mb, 24, 32, 4, 512, 256, 78)
+    for _ in range(3):
+        L.y.zero_()
+        graph.replay()
+        theirs = other.run().clone()
+        torch.cuda.synchronize()
+        assert torch.equal(L.y, eager)
+        assert torch.equal(other.run(), theirs)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_expert_training_step(mb, dtype):
+    """Forward and both gradients of the gate, up and down products of one step, against autograd in 64 bits on the same
+    16-bit values; the gradient by the tokens is the combine's sum of dx rows."""
+    say(f"training step {dtype}")
+    T, E, topk, H, F = 50, 12, 3, 256, 128
+    p = route(mb, T, E, topk, 91)
+    n = T * topk
+    off, tok = p["offsets"].cpu(), p["row_tok"].cpu()
+    g = torch.Generator().manual_seed(92)
+    x = torch.randn(T, H, generator=g).to(dtype)
+    w = (torch.randn(E, F, H, generator=g) / H ** 0.5).to(dtype)
+    dy = torch.randn(n, F, generator=g).to(dtype)
+    out = torch.empty(n, F, device="cuda")
+    mb.grouped_gemm(dev(x), dev(w), p["offsets"], out, row_tok=p["row_tok"])
+    dx = torch.empty(n, H, device="cuda")
+    mb.grouped_gemm_dx(dev(dy), dev(w), p["offsets"], dx)
+    dw = torch.empty(E, F, H, device="cuda")
+    mb.grouped_gemm_dw(dev(dy), dev(x), p["offsets"], dw, row_tok=p["row_tok"])
+    dtok = torch.empty(T, H, device="cuda")
+    mb.combine(dx, p["inv_pos"], T, topk, H, None, dtok)
+    x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+    y = torch.cat([x64[tok[a:b].long()] @ w64[e].T for e, a, b in gu.groups(off, n, E)])
+    (y * dy.double()).sum().backward()
+    my = torch.cat([x.double().abs()[tok[a:b].long()] @ w.double().abs()[e].T for e, a, b in gu.groups(off, n, E)])
+    assert bool(((out.cpu().double() - y).abs() <= gu.rounded(y, gu.sum_bound(my, H, 32), F32)).all())
+    mw = torch.stack([dy[a:b].double().abs().T @ x.double().abs()[tok[a:b].long()] for _, a, b in gu.groups(off, n, E)])
+    assert bool(((dw.cpu().double() - w64.grad).abs() <= gu.rounded(w64.grad, gu.sum_bound(mw, n, 32), F32)).all())
+    mx = torch.zeros(T, H, dtype=torch.float64)
+    rows = torch.cat([dy[a:b].double().abs() @ w[e].double().abs() for e, a, b in gu.groups(off, n, E)])
+    mx.index_add_(0, tok.long(), rows)
+    assert bool(((dtok.cpu().double() - x64.grad).abs() <= gu.sum_bound(mx, F, 32) + 4 * 2.0 ** -24 * mx).all())
+    # and against differences of the forward product: it is linear in x, so one central difference is exact
+    # up to rounding
+    i, j = 7, 11
+    step = 0.5
+    f = []
+    for d in (step, -step):
+        xp = x.float().clone()
+        xp[i, j] += d
+        moved = xp.to(dtype)
+        mb.grouped_gemm(dev(moved), dev(w), p["offsets"], out, row_tok=p["row_tok"])
+        f.append((float(moved[i, j]), float((out.cpu().double() * dy.double()).sum())))
+    slope = (f[0][1] - f[1][1]) / (f[0][0] - f[1][0])
+    # each of the two sums is off by at most the bound of its elements times dy
+    err = float((gu.sum_bound(my * 2, H, 32) * dy.double().abs()).sum()) * 2 / (f[0][0] - f[1][0])
+    assert abs(slope - float(dtok[i, j])) <= err
+
+
+def test_two_calls_on_two_streams(mb):
+    """Calls share nothing: two at once on two streams give what they give alone."""
+    say("two streams at once")
+    a, b = (MxLayer(mb, 64, 32, 4, 512, 256, 100 + i) for i in range(2))
+    ya, yb = a.run().clone(), b.run().clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for layer, s in zip((a, b), streams):
+            layer.run(stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.y, ya) and torch.equal(b.y, yb)
