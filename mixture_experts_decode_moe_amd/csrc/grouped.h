@@ -50,15 +50,4 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s);
 
-// Rows of group e, inside [0, n_rows) whatever the offsets hold.
-struct GroupRange {
-  int r0, n;
-};
-MOE_DEV GroupRange group_range(const GroupedArgs &a, int e) {
-  if (!a.offsets) return GroupRange{0, a.n_rows};
-  const int lo = min(max(a.offsets[e], 0), a.n_rows);
-  const int hi = min(max(a.offsets[e + 1], lo), a.n_rows);
-  return GroupRange{lo, hi - lo};
-}
-
 }  // namespace moe

@@ -50,23 +50,29 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // Direct loads: every lane's 16 (4) bytes go to LDS at `dst` + lane * 16 (4).
 // Written in assembly because the compiler would otherwise wait for them
 // before any LDS read of the same loop; they have no destination registers,
-// and the kernel waits for them itself.
+// and the kernel waits for them itself.  `dst` is the same in every lane.
 MOE_DEV void direct16(const char *p, uint32_t dst) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(p) : "memory", "m0");
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                       __builtin_amdgcn_readfirstlane(dst)),
+                   "v"(p) : "memory", "m0");
 }
 MOE_DEV void direct4(const char *p, uint32_t dst) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(dst), "v"(p) : "memory", "m0");
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
+                       __builtin_amdgcn_readfirstlane(dst)),
+                   "v"(p) : "memory", "m0");
 }
 MOE_DEV uint32_t lds_addr(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)p));
 }
 
-// XOR of the piece index of staged row R.  `a` rows are read in the order
-// 32 j + 8 i + 4 h + b (i, b = 0..3 over 16 lanes), `b` rows in order; a row is
-// half of the 64 banks, so rows that differ in bit 0 never collide and the
-// other three varying bits choose the piece.
-MOE_DEV int swz_a(int R) { return ((R >> 1) & 1) | (((R >> 3) & 3) << 1); }
-MOE_DEV int swz_b(int R) { return (R >> 1) & 7; }
+// XOR of the piece index of staged row R.  A row is half of the 64 banks, so
+// rows that differ in bit 0 never collide and the other three bits that vary
+// over 16 lanes choose the piece: rows in order, or (PAIRS) 32 j + 8 i + 4 h +
+// b with i, b = 0..3 over the lanes.
+template <bool PAIRS>
+MOE_DEV int swz(int R) {
+  return PAIRS ? ((R >> 1) & 1) | (((R >> 3) & 3) << 1) : (R >> 1) & 7;
+}
 // the same for transposed reads: eight rows of a half wave read 32 bytes each
 MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
 
@@ -87,36 +93,44 @@ MOE_DEV f32x4_t mfma_mx(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c, ui
                                                           static_cast<int>(sb));
 }
 
-// pre[e] = row tiles of the groups before e; pre[E] = all of them
+// Fills lo[e] (e = 0 .. E) with the groups' first rows, inside [0, n_rows]
+// whatever the offsets hold, and (BT > 0) pre[e] with the row tiles of the
+// groups before e, pre[E] = all of them.  Group e has max(lo[e + 1] - lo[e],
+// 0) rows.
 template <int BT>
-MOE_DEV void row_tiles(const GroupedArgs &a, int *pre, int *scratch) {
+MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch) {
   constexpr int kPer = kGrMaxExperts / kGrThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int cnt[kPer], mine = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    cnt[i] = e < a.E ? (group_range(a, e).n + BT - 1) / BT : 0;
-    mine += cnt[i];
-  }
-  int inc = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(inc, off);
-    if (lane >= off) inc += o;
-  }
-  if (lane == 63) scratch[wave] = inc;
+  for (int e = tid; e <= a.E; e += kGrThreads)
+    lo[e] = a.offsets ? min(max(a.offsets[e], 0), a.n_rows) : e * a.n_rows;  // without offsets E is 1
   lds_barrier();
-  int base = inc - mine;
-  for (int w = 0; w < wave; ++w) base += scratch[w];
+  if constexpr (BT > 0) {
+    int cnt[kPer], mine = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    if (e <= a.E) pre[e] = base;
-    base += cnt[i];
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      cnt[i] = e < a.E ? (max(lo[e + 1] - lo[e], 0) + BT - 1) / BT : 0;
+      mine += cnt[i];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 63) scratch[wave] = inc;
+    lds_barrier();
+    int base = inc - mine;
+    for (int w = 0; w < wave; ++w) base += scratch[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      if (e <= a.E) pre[e] = base;
+      base += cnt[i];
+    }
+    if (tid == kGrThreads - 1 && a.E == kGrMaxExperts) pre[kGrMaxExperts] = base;
+    lds_barrier();
   }
-  if (tid == kGrThreads - 1 && a.E == kGrMaxExperts) pre[kGrMaxExperts] = base;
-  lds_barrier();
 }
 
 // The expert of row tile j (pre[e] <= j < pre[e + 1]), found by the whole
@@ -128,44 +142,57 @@ MOE_DEV int tile_expert(const int *pre, int E, int j) {
   return 16 * c + __popcll(__ballot(lane < 16 && i < E && pre[i] <= j)) - 1;
 }
 
-// N (4 or 8) neighbouring columns of one output row
-template <int N>
-MOE_DEV void store_cols(const GroupedArgs &a, int64_t at, int col, const float (&v)[N]) {
-  const bool whole = a.out_vec && col + N <= a.na;
-  if (a.out_type == MOE_T_F32) {
-    float *o = reinterpret_cast<float *>(a.out) + at + col;
-    if (whole) {
+// Results on their way to memory: W words of one output row's neighbouring
+// columns, as they will be stored.
+template <int OUT, int W>
+struct Packed {
+  static constexpr int kCols = OUT == MOE_T_F32 ? W : 2 * W;
+  uint32_t w[W];
+  MOE_DEV void set(const float (&v)[kCols]) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (col + i < a.na) o[i] = v[i];
-    }
-    return;
-  }
-  uint32_t p[N / 2];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    if (a.out_type == MOE_T_BF16) {
-      p[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
-    } else {
-      const f32x2v_t f = {v[2 * i], v[2 * i + 1]};
-      p[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2_t));
+    for (int i = 0; i < W; ++i) {
+      if constexpr (OUT == MOE_T_F32) {
+        w[i] = __float_as_uint(v[i]);
+      } else if constexpr (OUT == MOE_T_BF16) {
+        w[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
+      } else {
+        const f32x2v_t f = {v[2 * i], v[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2_t));
+      }
     }
   }
-  uint16_t *o = reinterpret_cast<uint16_t *>(a.out) + at + col;
-  if (whole) {
-    if constexpr (N == 8)
-      *reinterpret_cast<uint4 *>(o) = make_uint4(p[0], p[1], p[2], p[3]);
-    else
-      *reinterpret_cast<uint2 *>(o) = make_uint2(p[0], p[1]);
-  } else {
+  // the lane that holds column chunk g of row l16 gives it to lane 4 l16 +
+  // g: four neighbouring lanes then store 16 W bytes of a row
+  MOE_DEV void by_row() {
+    const int from = 4 * ((lane_id() >> 2) + 16 * (lane_id() & 3));
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (col + i < a.na) o[i] = static_cast<uint16_t>(p[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < W; ++i) w[i] = __builtin_amdgcn_ds_bpermute(from, w[i]);
   }
-}
+  template <bool WHOLE>
+  MOE_DEV void store(const GroupedArgs &a, int64_t at, int col) const {
+    char *o = a.out + (at + col) * (OUT == MOE_T_F32 ? 4 : 2);
+    if (WHOLE || (a.out_vec && col + kCols <= a.na)) {
+      // fp32 results are written once and read by another launch: kept out of
+      // the caches' way (dw, 2.1 GB: 676 -> 604 us; 16-bit results are half
+      // the lines and lose, 233 -> 261 us for a 0.5 GB output)
+      if constexpr (OUT == MOE_T_F32)
+        __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t *>(o));
+      else if constexpr (W == 4)
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        if (col + i >= a.na) break;
+        if constexpr (OUT == MOE_T_F32)
+          reinterpret_cast<uint32_t *>(o)[i] = w[i];
+        else
+          reinterpret_cast<uint16_t *>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      }
+    }
+  }
+};
 
 // One operand's requests of this lane: piece i of step s is read at p[i] +
 // s * advance while s * unit < lim[i], else from the page of zeros.
@@ -175,19 +202,37 @@ struct Requests {
   int32_t lim[N];
 };
 
-template <int KIND, int TYPE, int BT, bool SWIGLU>
+// One output tile (the same in every lane).
+struct Tile {
+  int e, ct, bt;
+  int r0, n;   // the group's rows
+  int b_rows;  // output rows from the tile's first on
+  int steps;
+};
+
+template <int KIND, int TYPE, int OUT, int BT, bool SWIGLU>
 __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
   constexpr bool MX = KIND == kGroupedMx, DW = KIND == kGroupedDw;
   constexpr bool ACROSS_A = KIND == kGroupedDx || DW, ACROSS_B = DW;  // reduction across the operand's rows
   constexpr int NA = 4, NB = BT / 32;  // 1 KB requests a wave, a step
   constexpr int FB = BT / 32;          // 16-row fragments of a wave along b
-  constexpr int kUnit = ACROSS_A && ACROSS_B ? kGrRed : kGrStep;
+  constexpr int kCols = SWIGLU ? kGrCols / 2 : kGrCols;
   constexpr uint32_t kDataA = kGrCols * kGrStep, kDataB = BT * kGrStep;
   constexpr uint32_t kScale = MX ? (kGrCols + BT) * 8 : 0;
   constexpr uint32_t kBuf = kDataA + kDataB + kScale;
+  // The matrices' rows behind a lane's accumulators: fragments f and f + 1
+  // interleaved in fours where that makes eight neighbouring 16-bit columns
+  // a lane, else fragment by fragment.
+  constexpr bool kPairs = OUT != MOE_T_F32 && !ACROSS_A;
+  constexpr int kWords = OUT == MOE_T_F32 || kPairs ? 4 : 2;
+  constexpr int kChunks = (SWIGLU ? 2 : 4) / (kPairs ? 2 : 1);  // stores of a lane a row fragment
+  using Out = Packed<OUT, kWords>;
   static_assert(!DW || BT == kGrCols, "dw tiles are square");
   __shared__ __align__(1024) char lds[2 * kBuf];
-  __shared__ int pre[kGrMaxExperts + 1];
+  __shared__ float row_scale[2][BT];
+  constexpr int kTokens = DW ? kGrRed : BT;
+  __shared__ int row_token[2][kTokens];
+  __shared__ int lo[kGrMaxExperts + 1], pre[DW ? 1 : kGrMaxExperts + 1];
   __shared__ int scratch[kGrThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -195,58 +240,98 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
   const int l16 = lane & 15, g = lane >> 4;
   const char *zero = reinterpret_cast<const char *>(&g_zero_page);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const uint32_t token0 = __builtin_amdgcn_readfirstlane(lds_addr(row_token));
+  const uint32_t scale0 = __builtin_amdgcn_readfirstlane(lds_addr(row_scale));
 
-  int n_items;
-  if constexpr (DW) {
-    n_items = a.E * col_tiles * dw_tiles;
-  } else {
-    row_tiles<BT>(a, pre, scratch);
-    n_items = pre[a.E] * col_tiles;
-  }
+  group_table<DW ? 0 : BT>(a, lo, pre, scratch);
+  const int n_items = DW ? a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[DW ? 0 : a.E]) * col_tiles;
   // blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
   const int end = static_cast<int>(static_cast<int64_t>(n_items) * (xcd + 1) / 8);
-  for (int item = static_cast<int>(static_cast<int64_t>(n_items) * xcd / 8) + (blockIdx.x >> 3); item < end; item += per) {
-    int e, ct, bt;
-    if constexpr (DW) {
-      e = item / (col_tiles * dw_tiles);
-      const int in = item - e * (col_tiles * dw_tiles);
-      ct = in / dw_tiles;
-      bt = in - ct * dw_tiles;
-    } else {
-      e = __builtin_amdgcn_readfirstlane(tile_expert(pre, a.E, item / col_tiles));
-      const int mt = pre[e + 1] - pre[e];
-      const int in = item - pre[e] * col_tiles;
-      ct = in / mt;
-      bt = in - ct * mt;
-      if (bt < 0 || bt >= mt) continue;  // only where offsets overlap
-    }
-    const GroupRange gr = group_range(a, e);
-    const int b0 = bt * BT;                        // first output row of the tile
-    const int b_rows = (DW ? a.nb : gr.n) - b0;    // output rows from there on
-    const int c0 = ct * (SWIGLU ? kGrCols / 2 : kGrCols);
-    const int red = DW ? gr.n : a.red;             // rows (across) or bytes (along)
-    constexpr int kRedUnit = KIND == kGroupedDx ? kGrRed : kUnit;
-    const int steps = (red + kRedUnit - 1) / kRedUnit;
+  const int begin = static_cast<int>(static_cast<int64_t>(n_items) * xcd / 8) + (blockIdx.x >> 3);
 
-    Requests<NA> ra;
-    Requests<NB> rb;
-    const char *abase = a.a + static_cast<int64_t>(e) * a.a_expert;
-    const char *upbase = SWIGLU ? a.a2 + static_cast<int64_t>(e) * a.a_expert : nullptr;
+  auto locate = [&](int item) __attribute__((always_inline)) {
+    Tile t;
+    if constexpr (DW) {
+      t.e = item / (col_tiles * dw_tiles);
+      const int in = item - t.e * (col_tiles * dw_tiles);
+      t.bt = in / col_tiles;
+      t.ct = in - t.bt * col_tiles;
+    } else {
+      t.e = __builtin_amdgcn_readfirstlane(tile_expert(pre, a.E, item / col_tiles));
+      const int j = item / col_tiles;
+      t.ct = item - j * col_tiles;
+      t.bt = j - __builtin_amdgcn_readfirstlane(pre[t.e]);
+    }
+    t.r0 = __builtin_amdgcn_readfirstlane(lo[t.e]);
+    t.n = max(__builtin_amdgcn_readfirstlane(lo[t.e + 1]) - t.r0, 0);
+    t.b_rows = (DW ? a.nb : t.n) - t.bt * BT;
+    const int red = DW ? t.n : a.red;
+    constexpr int kUnit = ACROSS_A ? kGrRed : kGrStep;
+    t.steps = (red + kUnit - 1) / kUnit;
+    if (!DW && (t.bt < 0 || t.b_rows <= 0)) t.steps = 0;  // only where offsets overlap
+    return t;
+  };
+  // ---- The requesting side runs one step ahead of the products, across the
+  // tiles: while a tile's last step is multiplied and its results are
+  // stored, the next tile's first step is on its way.  The tokens of the
+  // rows that a request gathers are brought to LDS a step earlier still; they
+  // never pass through registers on the way, where the compiler would wait
+  // for them (and so for all requests before them).
+  int next = begin;  // item of the next request
+  int next_step = 0;
+  int tiles_begun = 0;
+  int slot = 0;  // of row_token: the next request's tokens
+  Tile nt{};
+  Requests<NA> ra;
+  Requests<NB> rb;
+  const char *sp[2] = {zero, zero};
+  int slim[2] = {INT32_MIN, INT32_MIN};
+  const bool gather = KIND != kGroupedDx && a.row_tok;
+
+  auto request_tokens = [&]() __attribute__((always_inline)) {
+    if (!gather || (!DW && next_step > 0)) return;
+    slot ^= 1;
+    if (64 * wave < kTokens) {
+      const int r = (DW ? next_step * kGrRed : nt.bt * BT) + 64 * wave + lane;
+      direct4(reinterpret_cast<const char *>(a.row_tok + nt.r0 + (r < nt.n ? r : 0)),
+              token0 + (slot * kTokens + 64 * wave) * 4);
+    }
+  };
+  // row of the gathered operand behind row r of the group, `at` of the
+  // request's; -1: none
+  auto source = [&](int r, int at) __attribute__((always_inline)) {
+    if (r >= nt.n) return -1;
+    if (!gather) return nt.r0 + r;
+    const int k = row_token[slot][at];
+    return static_cast<uint32_t>(k) < static_cast<uint32_t>(a.T) ? k : -1;
+  };
+  auto find_next = [&]() __attribute__((always_inline)) {
+    while (next < end) {
+      nt = locate(next);
+      if (nt.steps > 0) break;
+      next += per;
+    }
+    if (next < end) request_tokens();
+  };
+  // addresses of tile nt's requests
+  auto set_up = [&]() __attribute__((always_inline)) {
+    const int c0 = nt.ct * kCols, b0 = nt.bt * BT;
+    const int red = DW ? nt.n : a.red;
+    const char *abase = a.a + static_cast<int64_t>(nt.e) * a.a_expert;
+    const char *upbase = SWIGLU ? a.a2 + static_cast<int64_t>(nt.e) * a.a_expert : nullptr;
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       if constexpr (ACROSS_A) {
         const int R = 4 * (wave + 4 * i) + g;
         const int col = c0 + 8 * (l16 ^ swz_t(R));
         const bool ok = col < a.na;
-        if constexpr (DW)
-          ra.p[i] = a.a + 2 * static_cast<int64_t>(ok ? col : 0);  // the row is added a step at a time
-        else
-          ra.p[i] = abase + R * a.a_ld + 2 * static_cast<int64_t>(ok ? col : 0);
+        // dw: the row is added a step at a time
+        ra.p[i] = (DW ? a.a : abase + R * a.a_ld) + 2 * static_cast<int64_t>(ok ? col : 0);
         ra.lim[i] = ok ? red - R : INT32_MIN;
       } else {
         const int R = 8 * (wave + 4 * i) + (lane >> 3);
-        const int piece = (lane & 7) ^ swz_a(R);
+        const int piece = (lane & 7) ^ swz<kPairs>(R);
         // SwiGLU: 32 gate rows, then their 32 up rows, for each half of the tile
         const int col = SWIGLU ? c0 + 32 * (R >> 6) + (R & 31) : c0 + R;
         const char *base = SWIGLU && (R & 32) ? upbase : abase;
@@ -255,112 +340,113 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
         ra.lim[i] = ok ? red - 16 * piece : INT32_MIN;
       }
     }
-    // Row of x or dy behind grouped row r (inside the group), or -1
-    auto source = [&](int r) __attribute__((always_inline)) {
-      const int at = gr.r0 + r;
-      if (KIND == kGroupedDx || !a.row_tok) return at;
-      const int t = a.row_tok[at];
-      return static_cast<uint32_t>(t) < static_cast<uint32_t>(a.T) ? t : -1;
-    };
-    int tok[NA];  // dw: the x row of each request of the next step
-    auto next_rows = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        const int r = s * kGrRed + 4 * (wave + 4 * i) + g;
-        tok[i] = r < red ? source(r) : -1;
-      }
-    };
-    if constexpr (DW) next_rows(0);
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       if constexpr (ACROSS_B) {
         const int R = 4 * (wave + 4 * i) + g;
         const int col = b0 + 8 * (l16 ^ swz_t(R));
         const bool ok = col < a.nb;
-        rb.p[i] = a.b + (gr.r0 + static_cast<int64_t>(R)) * a.b_ld + 2 * static_cast<int64_t>(ok ? col : 0);
+        rb.p[i] = a.b + (nt.r0 + static_cast<int64_t>(R)) * a.b_ld + 2 * static_cast<int64_t>(ok ? col : 0);
         rb.lim[i] = ok ? red - R : INT32_MIN;
       } else {
         const int R = 8 * (wave + 4 * i) + (lane >> 3);
-        const int piece = (lane & 7) ^ swz_b(R);
-        const int src = R < b_rows ? source(b0 + R) : -1;
-        rb.p[i] = a.b + (src < 0 ? 0 : src) * a.b_ld + 16 * piece;
-        const int bytes = KIND == kGroupedDx ? 2 * red : red;
-        rb.lim[i] = src >= 0 ? bytes - 16 * piece : INT32_MIN;
+        const int piece = (lane & 7) ^ swz<false>(R);
+        const int src = source(b0 + R, R);
+        rb.p[i] = a.b + max(src, 0) * a.b_ld + 16 * piece;
+        rb.lim[i] = src >= 0 ? (KIND == kGroupedDx ? 2 * red : red) - 16 * piece : INT32_MIN;
       }
     }
-    // MXFP4: eight scale bytes a row and step, two 4-byte requests; request
-    // q of a wave covers 32 rows of a (q = 0) or b
-    const char *sp[2] = {zero, zero};
-    int slim[2] = {INT32_MIN, INT32_MIN};
+    // MXFP4: eight scale bytes a row and step, two 4-byte requests a lane,
+    // each request of a wave 32 rows of a or b
     if constexpr (MX) {
       const int j = 4 * (lane & 1);
       const int R = 32 * wave + (lane >> 1);
       const int col = SWIGLU ? c0 + 32 * (R >> 6) + (R & 31) : c0 + R;
       const char *base = SWIGLU && (R & 32) ? a.as2 : a.as;
-      if (col < a.na) {
-        sp[0] = base + (static_cast<int64_t>(e) * a.na + col) * a.s_ld + j;
-        slim[0] = a.s_ld - j;
-      }
-      const int src = R < BT && R < b_rows ? source(b0 + R) : -1;
-      if (src >= 0) {
-        sp[1] = a.bs + static_cast<int64_t>(src) * a.s_ld + j;
-        slim[1] = a.s_ld - j;
-      }
+      sp[0] = base + (static_cast<int64_t>(nt.e) * a.na + (col < a.na ? col : 0)) * a.s_ld + j;
+      slim[0] = col < a.na ? a.s_ld - j : INT32_MIN;
+      const int src = R < BT ? source(b0 + R, R) : -1;
+      sp[1] = a.bs + static_cast<int64_t>(max(src, 0)) * a.s_ld + j;
+      slim[1] = src >= 0 ? a.s_ld - j : INT32_MIN;
     }
+  };
+  // requests the next step into buffer `b`
+  auto issue = [&](int b) __attribute__((always_inline)) {
+    if (next >= end) return;
+    const int s = next_step;
+    const uint32_t buf = lds0 + b * kBuf;
+    if (s == 0) {
+      set_up();
+      if (!DW && a.row_w && 64 * wave < BT) {
+        const int r = 64 * wave + lane;
+        direct4(r < nt.b_rows ? reinterpret_cast<const char *>(a.row_w + nt.r0 + nt.bt * BT + r) : zero,
+                scale0 + ((tiles_begun & 1) * BT + 64 * wave) * 4);
+      }
+      ++tiles_begun;
+    }
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const char *p;
+      if constexpr (DW) {
+        const int at = 4 * (wave + 4 * i) + g;
+        const int src = source(s * kGrRed + at, at);
+        p = ra.lim[i] > s * kGrRed && src >= 0 ? ra.p[i] + src * a.a_ld : zero;
+      } else if constexpr (ACROSS_A)
+        p = ra.lim[i] > s * kGrRed ? ra.p[i] + s * (kGrRed * a.a_ld) : zero;
+      else
+        p = ra.lim[i] > s * kGrStep ? ra.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
+      direct16(p, buf + 1024 * (wave + 4 * i));
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const char *p;
+      if constexpr (ACROSS_B)
+        p = rb.lim[i] > s * kGrRed ? rb.p[i] + s * (kGrRed * a.b_ld) : zero;
+      else
+        p = rb.lim[i] > s * kGrStep ? rb.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
+      direct16(p, buf + kDataA + 1024 * (wave + 4 * i));
+    }
+    if constexpr (MX) {
+      direct4(slim[0] > 8 * s ? sp[0] + 8 * s : zero, buf + kDataA + kDataB + 256 * wave);
+      if (32 * wave < BT)
+        direct4(slim[1] > 8 * s ? sp[1] + 8 * s : zero, buf + kDataA + kDataB + kGrCols * 8 + 256 * wave);
+    }
+    if (++next_step == nt.steps) {
+      next_step = 0;
+      next += per;
+      find_next();
+    } else {
+      request_tokens();
+    }
+  };
 
-    auto issue = [&](int s) __attribute__((always_inline)) {
-      const uint32_t buf = lds0 + (s & 1) * kBuf;
-#pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        const char *p;
-        if constexpr (DW) {
-          p = ra.lim[i] > s * kGrRed && tok[i] >= 0 ? ra.p[i] + tok[i] * a.a_ld : zero;
-        } else if constexpr (ACROSS_A) {
-          p = ra.lim[i] > s * kGrRed ? ra.p[i] + s * (kGrRed * a.a_ld) : zero;
-        } else {
-          p = ra.lim[i] > s * kGrStep ? ra.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
-        }
-        direct16(p, buf + 1024 * (wave + 4 * i));
-      }
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const char *p;
-        if constexpr (ACROSS_B)
-          p = rb.lim[i] > s * kGrRed ? rb.p[i] + s * (kGrRed * a.b_ld) : zero;
-        else
-          p = rb.lim[i] > s * kGrStep ? rb.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
-        direct16(p, buf + kDataA + 1024 * (wave + 4 * i));
-      }
-      if constexpr (MX) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (q == 0 || 32 * wave < BT)
-            direct4(slim[q] > 8 * s ? sp[q] + 8 * s : zero,
-                    buf + kDataA + kDataB + (q == 0 ? 0u : kGrCols * 8u) + 256 * wave);
-      }
-    };
-
+  find_next();
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  lds_barrier();
+  issue(0);
+  int buf = 0;
+  int tiles_done = 0;
+  bool younger = false;  // the tile's first requests were followed by a whole tile's stores
+  for (int item = begin; item < end; item += per) {
+    const Tile t = locate(item);
     f32x4_t acc[4][FB];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int h = 0; h < FB; ++h) acc[f][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    lds_barrier();  // the previous item's operand reads are done
-    if (steps > 0) {
-      issue(0);
-      if constexpr (DW) next_rows(1);
-    }
-    for (int s = 0; s < steps; ++s) {
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    for (int s = 0; s < t.steps; ++s) {
+      // this step's requests have landed; requests and stores are counted in
+      // the order they were made, so the stores behind them may be under way
+      if (s == 0 && younger)
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(FB * kChunks));
+      else
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
       lds_barrier();
-      if (s + 1 < steps) {
-        issue(s + 1);
-        if constexpr (DW) next_rows(s + 2);
-      }
-      const char *ta = lds + (s & 1) * kBuf;
+      if (next < end) issue(buf ^ 1);
+      const char *ta = lds + buf * kBuf;
       const char *tb = ta + kDataA;
       const char *ts = tb + kDataB;
+      buf ^= 1;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         auto along = [&](const char *t, int R, int sw) __attribute__((always_inline)) {
@@ -390,8 +476,8 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
           if constexpr (ACROSS_A) {
             A[f] = across(ta, 64 * wa + 16 * f);
           } else {
-            const int R = 64 * wa + 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3);
-            A[f] = along(ta, R, swz_a(R));
+            const int R = 64 * wa + (kPairs ? 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3) : 16 * f + l16);
+            A[f] = along(ta, R, swz<kPairs>(R));
             if constexpr (MX) sa[f] = *reinterpret_cast<const uint32_t *>(ts + 8 * R + 4 * kk) >> (8 * g);
           }
         }
@@ -401,7 +487,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
           if constexpr (ACROSS_B) {
             B[h] = across(tb, wb * (BT / 2) + 16 * h);
           } else {
-            B[h] = along(tb, R, swz_b(R));
+            B[h] = along(tb, R, swz<false>(R));
             if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 8 * (kGrCols + R) + 4 * kk) >> (8 * g);
           }
         }
@@ -416,45 +502,46 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
           }
       }
     }
+    if (!DW && t.steps == 0) continue;
 
+    const float *scale = row_scale[tiles_done++ & 1];
+    auto store_tile = [&](auto whole_t) __attribute__((always_inline)) {
+      constexpr bool WHOLE = decltype(whole_t)::value != 0;
 #pragma unroll
-    for (int h = 0; h < FB; ++h) {
-      const int r = wb * (BT / 2) + 16 * h + l16;  // output row inside the tile
-      if (r >= b_rows) continue;
-      const int64_t row = DW ? static_cast<int64_t>(e) * a.nb + b0 + r : static_cast<int64_t>(gr.r0) + b0 + r;
-      const float w = !DW && a.row_w ? a.row_w[row] : 1.f;
-      const int64_t at = row * a.out_ld;
-      if constexpr (ACROSS_A) {
+      for (int h = 0; h < FB; ++h) {
+        const int r0 = wb * (BT / 2) + 16 * h;  // the fragment's first row in the tile
+        const float w = !DW && a.row_w ? scale[r0 + l16] : 1.f;
+        const int r = r0 + (lane >> 2);  // the row that this lane stores
+        const bool in = WHOLE || r < t.b_rows;
+        const int64_t at =
+            ((DW ? static_cast<int64_t>(t.e) * a.nb : static_cast<int64_t>(t.r0)) + t.bt * BT + r) * a.out_ld;
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int col = c0 + 64 * wa + 16 * f + 4 * g;
-          const float v[4] = {acc[f][h].x, acc[f][h].y, acc[f][h].z, acc[f][h].w};
-          if (col < a.na) store_cols<4>(a, at, col, v);
-        }
-      } else if constexpr (SWIGLU) {
-        const int col = c0 + 32 * wa + 8 * g;
-        float v[8];
+        for (int c = 0; c < kChunks; ++c) {
+          float v[Out::kCols];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float gv = acc[i >> 2][h][i & 3], uv = acc[2 + (i >> 2)][h][i & 3];
-          v[i] = w * (gv / (1.f + expf(-gv)) * uv);
-        }
-        if (col < a.na) store_cols<8>(a, at, col, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = c0 + 64 * wa + 32 * j + 8 * g;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = w * acc[2 * j + (i >> 2)][h][i & 3];
-          if (col < a.na) store_cols<8>(a, at, col, v);
+          for (int i = 0; i < Out::kCols; ++i) {
+            const int f = kPairs ? 2 * c + (i >> 2) : c;
+            v[i] = acc[f][h][i & 3];
+            if constexpr (SWIGLU) v[i] = v[i] / (1.f + expf(-v[i])) * acc[f + 2][h][i & 3];
+            v[i] *= w;
+          }
+          Out o;
+          o.set(v);
+          o.by_row();
+          const int col = t.ct * kCols + (SWIGLU ? 32 : 64) * wa + Out::kCols * (4 * c + (lane & 3));
+          if (WHOLE || (in && col < a.na)) o.template store<WHOLE>(a, at, col);
         }
       }
-    }
+    };
+    younger = a.out_vec && t.b_rows >= BT && (t.ct + 1) * kCols <= a.na;
+    if (younger)
+      store_tile(IntC<1>{});
+    else
+      store_tile(IntC<0>{});
   }
 }
 
-template <int KIND, int TYPE, int BT, bool SWIGLU>
+template <int KIND, int TYPE, int OUT, int BT, bool SWIGLU = false>
 hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
   const int32_t cols = SWIGLU ? kGrCols / 2 : kGrCols;
   const int32_t col_tiles = (a.na + cols - 1) / cols;
@@ -465,30 +552,44 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
   const int64_t items = tiles * col_tiles;
   const int64_t blocks = (items + 7) / 8 * 8;
   constexpr int64_t kMost = 512;  // two blocks a compute unit
-  grouped_tile_kernel<KIND, TYPE, BT, SWIGLU>
+  grouped_tile_kernel<KIND, TYPE, OUT, BT, SWIGLU>
       <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), kGrThreads, 0, s>>>(a, col_tiles, dw_tiles);
   return hipGetLastError();
 }
 
-template <int KIND, int TYPE, bool SWIGLU>
-hipError_t launch_rows(const GroupedArgs &a, hipStream_t s) {
-  return launch_tile<KIND, TYPE, 128, SWIGLU>(a, s);
+template <int KIND>
+hipError_t launch_16bit(const GroupedArgs &a, hipStream_t s) {
+  if (a.type == MOE_T_BF16)
+    return a.out_type == MOE_T_F32 ? launch_tile<KIND, MOE_T_BF16, MOE_T_F32, 128>(a, s)
+                                   : launch_tile<KIND, MOE_T_BF16, MOE_T_BF16, 128>(a, s);
+  return a.out_type == MOE_T_F32 ? launch_tile<KIND, MOE_T_F16, MOE_T_F32, 128>(a, s)
+                                 : launch_tile<KIND, MOE_T_F16, MOE_T_F16, 128>(a, s);
+}
+
+template <bool SWIGLU>
+hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
+  switch (a.out_type) {
+    case MOE_T_BF16:
+      return launch_tile<kGroupedMx, 0, MOE_T_BF16, 128, SWIGLU>(a, s);
+    case MOE_T_F16:
+      return launch_tile<kGroupedMx, 0, MOE_T_F16, 128, SWIGLU>(a, s);
+    default:
+      return launch_tile<kGroupedMx, 0, MOE_T_F32, 128, SWIGLU>(a, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s) {
-  const bool bf = a.type == MOE_T_BF16;
   switch (a.kind) {
     case kGroupedMx:
-      return a.a2 ? launch_rows<kGroupedMx, 0, true>(a, s) : launch_rows<kGroupedMx, 0, false>(a, s);
+      return a.a2 ? launch_mx<true>(a, s) : launch_mx<false>(a, s);
     case kGroupedDx:
-      return bf ? launch_rows<kGroupedDx, MOE_T_BF16, false>(a, s) : launch_rows<kGroupedDx, MOE_T_F16, false>(a, s);
+      return launch_16bit<kGroupedDx>(a, s);
     case kGroupedDw:
-      return bf ? launch_tile<kGroupedDw, MOE_T_BF16, 128, false>(a, s)
-                : launch_tile<kGroupedDw, MOE_T_F16, 128, false>(a, s);
+      return launch_16bit<kGroupedDw>(a, s);
     default:
-      return bf ? launch_rows<kGroupedFwd, MOE_T_BF16, false>(a, s) : launch_rows<kGroupedFwd, MOE_T_F16, false>(a, s);
+      return launch_16bit<kGroupedFwd>(a, s);
   }
 }
 
