@@ -19,7 +19,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["api.hip", "route.hip", "permute.hip", "expert_decode.hip", "expert_mfma.hip", "expert_prefill.hip", "down_combine.hip", "combine.hip", "noalloc.hip", "calib.hip",
-           "grouped_api.hip", "grouped_gemm.hip", "mx_quant.hip"]
+           "grouped_api.hip", "grouped_gemm.hip", "grouped_few.hip", "mx_quant.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -49,5 +49,7 @@ struct GroupedArgs {
   int32_t out_vec;       // out rows are 16-byte aligned
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s);
+// fwd and mx with few rows an expert
+hipError_t launch_grouped_few(const GroupedArgs &a, hipStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,84 @@
+// Device pieces shared by the grouped products' kernels: the matrix
+// instructions on 16-byte operands and the way results take to memory.
+#pragma once
+
+#include "grouped.h"
+#include "mfma_common.h"
+
+namespace moe {
+
+// what requests outside an operand read
+static __device__ const uint4 g_zero_page = {0u, 0u, 0u, 0u};
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+template <int TYPE>
+MOE_DEV f32x4_t mfma16(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c) {
+  if constexpr (TYPE == MOE_T_BF16)
+    return mfma_bf16(a, b, c);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// MXFP4: sa and sb hold the lane's scale byte in their low byte
+MOE_DEV f32x4_t mfma_mx(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c, uint32_t sa, uint32_t sb) {
+  const i32x8_t A = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
+  const i32x8_t B = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, static_cast<int>(sa), 0,
+                                                          static_cast<int>(sb));
+}
+
+// Results on their way to memory: W words of one output row's neighbouring
+// columns, as they will be stored.
+template <int OUT, int W>
+struct Packed {
+  static constexpr int kCols = OUT == MOE_T_F32 ? W : 2 * W;
+  uint32_t w[W];
+  MOE_DEV void set(const float (&v)[kCols]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (OUT == MOE_T_F32) {
+        w[i] = __float_as_uint(v[i]);
+      } else if constexpr (OUT == MOE_T_BF16) {
+        w[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
+      } else {
+        const f32x2v_t f = {v[2 * i], v[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2_t));
+      }
+    }
+  }
+  // the lane that holds column chunk g of row l16 gives it to lane 4 l16 +
+  // g: four neighbouring lanes then store 16 W bytes of a row
+  MOE_DEV void by_row() {
+    const int from = 4 * ((lane_id() >> 2) + 16 * (lane_id() & 3));
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __builtin_amdgcn_ds_bpermute(from, w[i]);
+  }
+  template <bool WHOLE>
+  MOE_DEV void store(const GroupedArgs &a, int64_t at, int col) const {
+    char *o = a.out + (at + col) * (OUT == MOE_T_F32 ? 4 : 2);
+    if (WHOLE || (a.out_vec && col + kCols <= a.na)) {
+      // fp32 results are written once and read by another launch: kept out of
+      // the caches' way (dw, 2.1 GB: 676 -> 604 us; 16-bit results are half
+      // the lines and lose, 233 -> 261 us for a 0.5 GB output)
+      if constexpr (OUT == MOE_T_F32)
+        __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t *>(o));
+      else if constexpr (W == 4)
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        if (col + i >= a.na) break;
+        if constexpr (OUT == MOE_T_F32)
+          reinterpret_cast<uint32_t *>(o)[i] = w[i];
+        else
+          reinterpret_cast<uint16_t *>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      }
+    }
+  }
+};
+
+}  // namespace moe

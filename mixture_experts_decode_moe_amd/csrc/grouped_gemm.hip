@@ -29,9 +29,7 @@
 // A block of four waves (2 x 2) loops over items (expert, column tile, row
 // tile); the row tiles of one column tile follow one another, so a matrix
 // tile comes from HBM once, and each XCD works on its own range of items.
-#include "grouped.h"
-
-#include "mfma_common.h"
+#include "grouped_device.h"
 
 namespace moe {
 
@@ -42,10 +40,6 @@ constexpr int kGrMaxExperts = 1024;
 constexpr int kGrCols = 128;  // rows of the `a` tile
 constexpr int kGrStep = 128;  // bytes of a row a step (reduction along rows)
 constexpr int kGrRed = 64;    // rows a step (reduction across rows)
-
-__device__ const uint4 g_zero_page = {0u, 0u, 0u, 0u};
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // Direct loads: every lane's 16 (4) bytes go to LDS at `dst` + lane * 16 (4).
 // Written in assembly because the compiler would otherwise wait for them
@@ -75,23 +69,6 @@ MOE_DEV int swz(int R) {
 }
 // the same for transposed reads: eight rows of a half wave read 32 bytes each
 MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
-
-template <int TYPE>
-MOE_DEV f32x4_t mfma16(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c) {
-  if constexpr (TYPE == MOE_T_BF16)
-    return mfma_bf16(a, b, c);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
-                                                  0, 0);
-}
-
-// MXFP4: sa and sb hold the lane's scale byte in their low byte
-MOE_DEV f32x4_t mfma_mx(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c, uint32_t sa, uint32_t sb) {
-  const i32x8_t A = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
-  const i32x8_t B = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, static_cast<int>(sa), 0,
-                                                          static_cast<int>(sb));
-}
 
 // Fills lo[e] (e = 0 .. E) with the groups' first rows, inside [0, n_rows]
 // whatever the offsets hold, and (BT > 0) pre[e] with the row tiles of the
@@ -141,58 +118,6 @@ MOE_DEV int tile_expert(const int *pre, int E, int j) {
   const int i = 16 * c + (lane & 15);
   return 16 * c + __popcll(__ballot(lane < 16 && i < E && pre[i] <= j)) - 1;
 }
-
-// Results on their way to memory: W words of one output row's neighbouring
-// columns, as they will be stored.
-template <int OUT, int W>
-struct Packed {
-  static constexpr int kCols = OUT == MOE_T_F32 ? W : 2 * W;
-  uint32_t w[W];
-  MOE_DEV void set(const float (&v)[kCols]) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if constexpr (OUT == MOE_T_F32) {
-        w[i] = __float_as_uint(v[i]);
-      } else if constexpr (OUT == MOE_T_BF16) {
-        w[i] = f32x2_to_bf16x2_rne(v[2 * i], v[2 * i + 1]);
-      } else {
-        const f32x2v_t f = {v[2 * i], v[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2_t));
-      }
-    }
-  }
-  // the lane that holds column chunk g of row l16 gives it to lane 4 l16 +
-  // g: four neighbouring lanes then store 16 W bytes of a row
-  MOE_DEV void by_row() {
-    const int from = 4 * ((lane_id() >> 2) + 16 * (lane_id() & 3));
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __builtin_amdgcn_ds_bpermute(from, w[i]);
-  }
-  template <bool WHOLE>
-  MOE_DEV void store(const GroupedArgs &a, int64_t at, int col) const {
-    char *o = a.out + (at + col) * (OUT == MOE_T_F32 ? 4 : 2);
-    if (WHOLE || (a.out_vec && col + kCols <= a.na)) {
-      // fp32 results are written once and read by another launch: kept out of
-      // the caches' way (dw, 2.1 GB: 676 -> 604 us; 16-bit results are half
-      // the lines and lose, 233 -> 261 us for a 0.5 GB output)
-      if constexpr (OUT == MOE_T_F32)
-        __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t *>(o));
-      else if constexpr (W == 4)
-        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
-        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        if (col + i >= a.na) break;
-        if constexpr (OUT == MOE_T_F32)
-          reinterpret_cast<uint32_t *>(o)[i] = w[i];
-        else
-          reinterpret_cast<uint16_t *>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-      }
-    }
-  }
-};
 
 // One operand's requests of this lane: piece i of step s is read at p[i] +
 // s * advance while s * unit < lim[i], else from the page of zeros.
@@ -578,9 +503,25 @@ hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
   }
 }
 
+// Whether the few-row kernel takes the call: up to 256 rows, and tiles for
+// less than one block a compute unit.  Below that the tiles leave most of the
+// chip idle and a tile's long walk is the whole time: one row each of eight
+// experts of 1024 x 2048 in 16 bits 27.9 us against 12.2, one row of a single
+// 1024 x 1024 matrix 15.7 against 4.8, 256 rows of it 15.9 against 10.3.  Above
+// it the tiles read every matrix once: 64 experts of 1024 x 1024, a row each,
+// 29.8 against 32.4 us, MXFP4 12.0 against 20.0; 1024 rows of one matrix 17.0
+// against 34.3.
+bool few_rows(const GroupedArgs &a) {
+  if (a.kind != kGroupedFwd && a.kind != kGroupedMx) return false;
+  const int32_t cols = a.a2 ? kGrCols / 2 : kGrCols;
+  const int32_t tiles = a.n_rows / 128 + (a.E < a.n_rows ? a.E : a.n_rows);
+  return a.n_rows <= 256 && static_cast<int64_t>(tiles) * ((a.na + cols - 1) / cols) <= 256;
+}
+
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s) {
+  if (few_rows(a)) return launch_grouped_few(a, s);
   switch (a.kind) {
     case kGroupedMx:
       return a.a2 ? launch_mx<true>(a, s) : launch_mx<false>(a, s);
