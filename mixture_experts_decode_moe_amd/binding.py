@@ -339,16 +339,20 @@ def mx_cols(cols: int) -> int:
     return -(-cols // 128) * 128
 
 
+# The small calls below are launch-bound, so their checks stay light: devices are compared by index and the current
+# stream is asked for by the raw handle (torch.cuda.current_stream builds a Stream object, about 3 us a call).
+
 def _rows(t, name):
-    """A matrix whose rows are contiguous (any row stride): (pointer, row stride, rows, columns, type)."""
+    """A matrix whose rows are contiguous (any row stride): (pointer, row stride, rows, columns, type, device index)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a device tensor")
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a matrix")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a device tensor")
     (rows, cols), (ld, step) = t.shape, t.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: expected contiguous rows")
     if rows <= 1:
         ld = max(ld, cols)  # the stride of a single row says nothing
@@ -357,95 +361,84 @@ def _rows(t, name):
     kind = DTYPES.get(t.dtype)
     if kind is None:
         raise ValueError(f"{name}: expected bfloat16, float16 or float32")
-    return t.data_ptr(), ld, rows, cols, kind
+    return t.data_ptr(), ld, rows, cols, kind, dev
 
 
 def _dense(t, name, dtype, n, dev):
-    """A contiguous device array of at least n values, or None."""
+    """Pointer of a contiguous array of at least n values on device `dev`, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() < n:
-        raise ValueError(f"{name}: expected {n} values of {dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on another device")
-    return _ptr(t)
+    if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous values of {dtype} on the other operands' device")
+    return t.data_ptr()
 
 
 def _mx(m, name, rows, cols, dev):
     """The C struct of MXFP4 rows (q, s)."""
     p = mx_cols(cols)
     q, s = m
-    return MoeMxRows(_dense(q, name + " codes", torch.uint8, rows * (p // 2), dev),
-                     _dense(s, name + " scales", torch.uint8, rows * (p // 32), dev))
+    return MoeMxRows(_dense(q, name, torch.uint8, rows * (p // 2), dev), _dense(s, name, torch.uint8, rows * (p // 32), dev))
 
 
-def _same_type(kind, others, what):
-    if any(k != kind for k in others):
-        raise ValueError(f"{what} have to be of one 16-bit type")
+def _weights(w, name, dev):
+    """[E][N][K] contiguous matrices: (pointer, E, N, K, type)."""
+    kind = DTYPES.get(w.dtype)
+    if w.dim() != 3 or kind is None or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous [E][N][K] of bfloat16, float16 or float32 on the rows' device")
+    return (w.data_ptr(), *w.shape, kind)
 
 
 def _call(fn, dev, stream, *args):
-    """Runs an entry point with `dev` current (its stream and launches belong to that device)."""
-    f = getattr(_lib, fn)
-    if dev.index == torch.cuda.current_device():
-        rc = f(*args, _stream(stream))
+    """Runs an entry point on `stream` (the current one of device `dev` by default) with `dev` current."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        rc = getattr(_lib, fn)(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, _stream(stream))
-    _check(fn, rc)
+            rc = getattr(_lib, fn)(*args, handle)
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
 
 
 def mx_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
     """moe_mx_quantize: rows of x [rows][cols] (bfloat16, float16 or float32, any row stride) to codes q uint8
     [rows][mx_cols(cols) / 2] and scales s uint8 [rows][mx_cols(cols) / 32]."""
-    xp, ld, rows, cols, kind = _rows(x, "x")
-    m = _mx((q, s), "x", rows, cols, x.device)
-    _call("moe_mx_quantize", x.device, stream, xp, kind, ld, rows, cols, m.q, m.s)
+    xp, ld, rows, cols, kind, dev = _rows(x, "x")
+    p = mx_cols(cols)
+    _call("moe_mx_quantize", dev, stream, xp, kind, ld, rows, cols, _dense(q, "q", torch.uint8, rows * (p // 2), dev),
+          _dense(s, "s", torch.uint8, rows * (p // 32), dev))
 
 
 def mx_dequantize(q: torch.Tensor, s: torch.Tensor, out: torch.Tensor, stream=None):
     """moe_mx_dequantize: the values of MXFP4 rows into out [rows][cols]."""
-    op, ld, rows, cols, kind = _rows(out, "out")
-    m = _mx((q, s), "out", rows, cols, out.device)
-    _call("moe_mx_dequantize", out.device, stream, m.q, m.s, rows, cols, op, kind, ld)
+    op, ld, rows, cols, kind, dev = _rows(out, "out")
+    p = mx_cols(cols)
+    _call("moe_mx_dequantize", dev, stream, _dense(q, "q", torch.uint8, rows * (p // 2), dev),
+          _dense(s, "s", torch.uint8, rows * (p // 32), dev), rows, cols, op, kind, ld)
 
 
 def mx_grouped_gemm(x, w, n_experts: int, K: int, offsets, out: torch.Tensor, up=None, row_tok=None, row_w=None,
                     stream=None):
     """moe_mx_grouped_gemm: out [n_rows][N] from MXFP4 pairs (codes, scales): x (T rows), w and up (n_experts * N
     rows) of K columns each.  offsets int32 [n_experts + 1] or None (one expert)."""
-    op, ld, n_rows, N, kind = _rows(out, "out")
-    dev = out.device
-    T = x[0].numel() // (mx_cols(K) // 2)
+    op, ld, n_rows, N, kind, dev = _rows(out, "out")
+    T = x[0].numel() // max(1, mx_cols(K) // 2)
     xm, wm = _mx(x, "x", T, K, dev), _mx(w, "w", n_experts * N, K, dev)
-    um = None if up is None else _mx(up, "up", n_experts * N, K, dev)
-    _call("moe_mx_grouped_gemm", dev, stream, ctypes.byref(xm), T, n_rows, ctypes.byref(wm),
-          None if um is None else ctypes.byref(um), n_experts, N, K,
+    um = None if up is None else ctypes.byref(_mx(up, "up", n_experts * N, K, dev))
+    _call("moe_mx_grouped_gemm", dev, stream, ctypes.byref(xm), T, n_rows, ctypes.byref(wm), um, n_experts, N, K,
           _dense(offsets, "offsets", torch.int32, n_experts + 1, dev),
           _dense(row_tok, "row_tok", torch.int32, n_rows, dev), _dense(row_w, "row_w", torch.float32, n_rows, dev),
           op, kind, ld)
 
 
-def _weights(w, name, dev):
-    """[E][N][K] contiguous matrices: (pointer, E, N, K, type)."""
-    if w.dim() != 3 or w.device != dev:
-        raise ValueError(f"{name}: expected [E][N][K] on the rows' device")
-    kind = DTYPES.get(w.dtype)
-    if kind is None:
-        raise ValueError(f"{name}: expected bfloat16, float16 or float32")
-    return (_ptr(w), *w.shape, kind)
-
-
 def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets, out: torch.Tensor, row_tok=None, row_w=None, stream=None):
     """moe_grouped_gemm: out [n_rows][N] from rows x [T][K] and matrices w [E][N][K] of one 16-bit type; out of that
     type or float32."""
-    xp, x_ld, T, K, kind = _rows(x, "x")
-    dev = x.device
+    xp, x_ld, T, K, kind, dev = _rows(x, "x")
     wp, E, N, wk, wkind = _weights(w, "w", dev)
-    op, out_ld, n_rows, on, okind = _rows(out, "out")
-    _same_type(kind, (wkind,), "x and w")
-    if wk != K or on != N or out.device != dev:
-        raise ValueError("x [T][K], w [E][N][K] and out [n_rows][N] do not fit")
+    op, out_ld, n_rows, on, okind, odev = _rows(out, "out")
+    if wkind != kind or wk != K or on != N or odev != dev:
+        raise ValueError("x [T][K], w [E][N][K] (of one type) and out [n_rows][N] do not fit")
     _call("moe_grouped_gemm", dev, stream, xp, x_ld, T, n_rows, wp, kind, E, N, K,
           _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),
           _dense(row_w, "row_w", torch.float32, n_rows, dev), op, okind, out_ld)
@@ -453,26 +446,22 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets, out: torch.Tensor, r
 
 def grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, offsets, dx: torch.Tensor, stream=None):
     """moe_grouped_gemm_dx: dx [n_rows][K] from dy [n_rows][N] and w [E][N][K]."""
-    yp, y_ld, n_rows, N, kind = _rows(dy, "dy")
-    dev = dy.device
+    yp, y_ld, n_rows, N, kind, dev = _rows(dy, "dy")
     wp, E, wn, K, wkind = _weights(w, "w", dev)
-    op, out_ld, rows, ok, okind = _rows(dx, "dx")
-    _same_type(kind, (wkind,), "dy and w")
-    if wn != N or ok != K or rows != n_rows or dx.device != dev:
-        raise ValueError("dy [n_rows][N], w [E][N][K] and dx [n_rows][K] do not fit")
+    op, out_ld, rows, ok, okind, odev = _rows(dx, "dx")
+    if wkind != kind or wn != N or ok != K or rows != n_rows or odev != dev:
+        raise ValueError("dy [n_rows][N], w [E][N][K] (of one type) and dx [n_rows][K] do not fit")
     _call("moe_grouped_gemm_dx", dev, stream, yp, y_ld, n_rows, wp, kind, E, N, K,
           _dense(offsets, "offsets", torch.int32, E + 1, dev), op, okind, out_ld)
 
 
 def grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, offsets, dw: torch.Tensor, row_tok=None, stream=None):
     """moe_grouped_gemm_dw: dw [E][N][K] from dy [n_rows][N] and rows x [T][K]."""
-    yp, y_ld, n_rows, N, kind = _rows(dy, "dy")
-    dev = dy.device
-    xp, x_ld, T, K, xkind = _rows(x, "x")
+    yp, y_ld, n_rows, N, kind, dev = _rows(dy, "dy")
+    xp, x_ld, T, K, xkind, xdev = _rows(x, "x")
     op, E, on, ok, okind = _weights(dw, "dw", dev)
-    _same_type(kind, (xkind,), "dy and x")
-    if on != N or ok != K or x.device != dev:
-        raise ValueError("dy [n_rows][N], x [T][K] and dw [E][N][K] do not fit")
+    if xkind != kind or on != N or ok != K or xdev != dev:
+        raise ValueError("dy [n_rows][N], x [T][K] (of one type) and dw [E][N][K] do not fit")
     _call("moe_grouped_gemm_dw", dev, stream, yp, y_ld, xp, x_ld, T, n_rows, kind, E, N, K,
           _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),
           op, okind)
