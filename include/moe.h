@@ -331,7 +331,8 @@ int moe_layer_forward_noalloc(const moe_layer *L, const uint16_t *x_bf16, int32_
  * belong to expert e (int32 [E+1] on the device; NULL with E == 1: all
  * n_rows rows).  Offsets are taken as between 0 and n_rows.  Rows of `out`
  * outside every group are left as they were.  Groups may be empty and of
- * any length.  E <= 1024.  Sums are held in fp32.
+ * any length.  E <= 1024; E * (n_rows / 128 + 1) * (max(N, K) / 64 + 1)
+ * below 2^30.  Sums are held in fp32.
  *
  * row_tok int32 [n_rows] or NULL: row r reads row row_tok[r] of x, which
  * has T rows; a value outside [0, T) reads a row of zeros.  NULL: row r
@@ -385,8 +386,8 @@ int moe_mx_grouped_gemm(const moe_mx_rows *x, int32_t T, int32_t n_rows, const m
 /* Grouped product in 16 bits: out[r][n] = row_w[r] * sum_k x[r][k]
  * w_e[n][k].  x rows and w [E][N][K] (dense) of type `type` (BF16 or F16);
  * out_type = type or F32.  N and K multiples of 8 up to 65536; inputs
- * 16-byte aligned with strides that are multiples of 8 elements; out
- * 16-byte aligned, its stride a multiple of 8.  n_rows = 0 is a no-op. */
+ * 16-byte aligned with strides that are multiples of 8 elements up to 2^24;
+ * out likewise.  n_rows = 0 is a no-op. */
 int moe_grouped_gemm(const void *x, int64_t x_ld, int32_t T, int32_t n_rows, const void *w, int32_t type, int32_t E,
                      int32_t N, int32_t K, const int32_t *offsets, const int32_t *row_tok, const float *row_w,
                      void *out, int32_t out_type, int64_t out_ld, void *stream);

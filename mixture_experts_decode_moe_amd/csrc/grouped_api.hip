@@ -11,7 +11,8 @@ namespace {
 
 constexpr int32_t kMaxWidth = 65536;         // N and K
 constexpr int32_t kMaxRows = INT32_MAX / 2;  // as moe_permute
-constexpr int kMinTileRows = 16, kMinTileCols = 16;
+constexpr int64_t kMaxStride = 1 << 24;      // of 16-bit operands: a step's rows are addressed in 32 bits
+constexpr int kTileRows = 128, kTileCols = 64;  // the smallest tiles of the kernels that count so
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -27,10 +28,10 @@ int check_groups(int32_t n_rows, int32_t E, int32_t N, int32_t K, const int32_t 
   if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
   if (!aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || N > kMaxWidth || K > kMaxWidth || n_rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
-  // items are counted in 32 bits
-  const int64_t tiles = n_rows / kMinTileRows + static_cast<int64_t>(E);
-  const int64_t cols = (N > K ? N : K) / kMinTileCols + 1;
-  return tiles * cols > INT32_MAX ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  // tiles are counted in 32 bits, whatever the offsets hold
+  const int64_t tiles = E * (n_rows / kTileRows + static_cast<int64_t>(1));
+  const int64_t cols = (N > K ? N : K) / kTileCols + 1;
+  return tiles * cols > INT32_MAX / 2 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // Rows that are gathered from T source rows.
@@ -44,7 +45,7 @@ int check_rows(const void *x, int32_t T, int32_t n_rows, const int32_t *row_tok,
 // A 16-bit operand's rows: whole 16-byte pieces.
 int check_operand(const void *p, int64_t ld, int32_t width) {
   if (ld < width || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
-  return ld % 8 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return ld % 8 || ld > kMaxStride ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 int check_16bit(int32_t type, int32_t out_type, int32_t N, int32_t K) {

@@ -12,6 +12,21 @@ static __device__ const uint4 g_zero_page = {0u, 0u, 0u, 0u};
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
+template <int CTRL, int ROWS>
+MOE_DEV int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// inclusive sum over the lanes before and including this one
+MOE_DEV int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
 template <int TYPE>
 MOE_DEV f32x4_t mfma16(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c) {
   if constexpr (TYPE == MOE_T_BF16)
@@ -28,6 +43,12 @@ MOE_DEV f32x4_t mfma_mx(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c, ui
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, static_cast<int>(sa), 0,
                                                           static_cast<int>(sb));
 }
+
+// silu(g) * u with the chip's exponential and reciprocal: a few units in
+// the last place of fp32, 6 instructions for 29 of expf and a division (a
+// tile's epilogue 6500 -> 2600 cycles).  exp(-g) overflows to infinity and
+// the reciprocal to 0 as in the exact form; -inf gives NaN as 0 * inf does.
+MOE_DEV float swiglu(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
 // Results on their way to memory: W words of one output row's neighbouring
 // columns, as they will be stored.
@@ -59,12 +80,10 @@ struct Packed {
   MOE_DEV void store(const GroupedArgs &a, int64_t at, int col) const {
     char *o = a.out + (at + col) * (OUT == MOE_T_F32 ? 4 : 2);
     if (WHOLE || (a.out_vec && col + kCols <= a.na)) {
-      // fp32 results are written once and read by another launch: kept out of
-      // the caches' way (dw, 2.1 GB: 676 -> 604 us; 16-bit results are half
-      // the lines and lose, 233 -> 261 us for a 0.5 GB output)
-      if constexpr (OUT == MOE_T_F32)
-        __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_t *>(o));
-      else if constexpr (W == 4)
+      // through the caches: stores past them (nontemporal) halve dw's rate
+      // where there is little to read (512 rows over 256 experts of 1024 x
+      // 2048: 342 against 565 us; 32768 rows: 520 against 603)
+      if constexpr (W == 4)
         *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
       else
         *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);

@@ -27,21 +27,6 @@ constexpr int kUnroll = 4;
 constexpr int kStepBytes = 64;  // of a row
 constexpr int kMaxBlocks = 256 * 8;
 
-template <int CTRL, int ROWS>
-MOE_DEV int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-// inclusive sum over the lanes before and including this one
-MOE_DEV int wave_scan(int v) {
-  v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
-  v = dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
-  return v;
-}
-
 // 16 rows of one expert
 struct RowTile {
   int e, r0, n;  // n: rows from r0 to the group's end, 0: no such tile
@@ -208,7 +193,7 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = acc[0][i];
-        if constexpr (SWIGLU) v[i] = v[i] / (1.f + expf(-v[i])) * acc[kMats - 1][i];
+        if constexpr (SWIGLU) v[i] = swiglu(v[i], acc[kMats - 1][i]);
         v[i] *= rw;
       }
       Packed<OUT, OUT == MOE_T_F32 ? 4 : 2> o;

@@ -20,26 +20,32 @@
 // transposing load (ds_read_b64_tr_b16: 16 lanes take a 4 x 16 patch and get
 // a column of four each).
 //
-// Staging is direct loads into LDS (no registers), one step ahead, two
-// buffers.  Requests that would leave the matrix, the group or the reduction
-// read a page of zeros instead, so tails need no masks in the product and
-// never meet another group's NaN.  The pieces of a row are permuted by an XOR
-// with row bits so that operand reads meet every bank equally.
+// Staging is direct loads into LDS (no registers), one or two steps ahead.
+// What lies past the end of the reduction reads a page of zeros, so that tails
+// need no masks in the product and never meet another group's NaN.  The pieces
+// of a row are permuted by an XOR with row bits so that operand reads meet the
+// banks equally.
 //
-// A block of four waves (2 x 2) loops over items (expert, column tile, row
-// tile); the row tiles of one column tile follow one another, so a matrix
-// tile comes from HBM once, and each XCD works on its own range of items.
+// A block loops over tiles (expert, 128 rows, 128 or 256 columns); a wave has
+// 64 x 64 results.  The column tiles of a row tile follow one another and each
+// XCD works on its own range of them, so that a group's rows and an expert's
+// matrix are shared in its L2.
+//
+// What bounds it: at the sizes of a layer every product is a stream of the
+// matrices and the results through HBM (wide tiles 4.5 to 5.0 TB/s of reads
+// with the rows beside them, dw 4.3 TB/s mostly of stores); a single 2048 x
+// 2048 matrix with 32768 rows reaches 960 TFLOP/s in bf16.
 #include "grouped_device.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kGrThreads = 256;
 constexpr int kGrMaxExperts = 1024;
-constexpr int kGrCols = 128;  // rows of the `a` tile
+constexpr int kGrRows = 128;  // output rows of a tile
 constexpr int kGrStep = 128;  // bytes of a row a step (reduction along rows)
 constexpr int kGrRed = 64;    // rows a step (reduction across rows)
+constexpr int kTableTiles = 32;
 
 // Direct loads: every lane's 16 (4) bytes go to LDS at `dst` + lane * 16 (4).
 // Written in assembly because the compiler would otherwise wait for them
@@ -50,10 +56,23 @@ MOE_DEV void direct16(const char *p, uint32_t dst) {
                        __builtin_amdgcn_readfirstlane(dst)),
                    "v"(p) : "memory", "m0");
 }
+// the same from a base that is the same in every lane and a 32-bit offset
+MOE_DEV void direct16(const char *base, uint32_t off, uint32_t dst) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                       __builtin_amdgcn_readfirstlane(dst)),
+                   "v"(off), "s"(uniform_gptr(base))
+                   : "memory", "m0");
+}
 MOE_DEV void direct4(const char *p, uint32_t dst) {
   __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
                        __builtin_amdgcn_readfirstlane(dst)),
                    "v"(p) : "memory", "m0");
+}
+MOE_DEV void direct4(const char *base, uint32_t off, uint32_t dst) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                       __builtin_amdgcn_readfirstlane(dst)),
+                   "v"(off), "s"(uniform_gptr(base))
+                   : "memory", "m0");
 }
 MOE_DEV uint32_t lds_addr(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)p));
@@ -71,30 +90,25 @@ MOE_DEV int swz(int R) {
 MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
 
 // Fills lo[e] (e = 0 .. E) with the groups' first rows, inside [0, n_rows]
-// whatever the offsets hold, and (BT > 0) pre[e] with the row tiles of the
+// whatever the offsets hold, and (PRE) pre[e] with the row tiles of the
 // groups before e, pre[E] = all of them.  Group e has max(lo[e + 1] - lo[e],
 // 0) rows.
-template <int BT>
+template <bool PRE, int NT>
 MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch) {
-  constexpr int kPer = kGrMaxExperts / kGrThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= a.E; e += kGrThreads)
+  for (int e = tid; e <= a.E; e += NT)
     lo[e] = a.offsets ? min(max(a.offsets[e], 0), a.n_rows) : e * a.n_rows;  // without offsets E is 1
   lds_barrier();
-  if constexpr (BT > 0) {
+  if constexpr (PRE) {
+    constexpr int kPer = kGrMaxExperts / NT;
     int cnt[kPer], mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid * kPer + i;
-      cnt[i] = e < a.E ? (max(lo[e + 1] - lo[e], 0) + BT - 1) / BT : 0;
+      cnt[i] = e < a.E ? (max(lo[e + 1] - lo[e], 0) + kGrRows - 1) / kGrRows : 0;
       mine += cnt[i];
     }
-    int inc = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(inc, off);
-      if (lane >= off) inc += o;
-    }
+    const int inc = wave_scan(mine);
     if (lane == 63) scratch[wave] = inc;
     lds_barrier();
     int base = inc - mine;
@@ -105,27 +119,10 @@ MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch) 
       if (e <= a.E) pre[e] = base;
       base += cnt[i];
     }
-    if (tid == kGrThreads - 1 && a.E == kGrMaxExperts) pre[kGrMaxExperts] = base;
+    if (tid == NT - 1 && a.E == kGrMaxExperts) pre[kGrMaxExperts] = base;
     lds_barrier();
   }
 }
-
-// The expert of row tile j (pre[e] <= j < pre[e + 1]), found by the whole
-// wave: among every 16th entry, then among those 16.
-MOE_DEV int tile_expert(const int *pre, int E, int j) {
-  const int lane = lane_id();
-  const int c = __popcll(__ballot(16 * lane < E && pre[16 * lane] <= j)) - 1;
-  const int i = 16 * c + (lane & 15);
-  return 16 * c + __popcll(__ballot(lane < 16 && i < E && pre[i] <= j)) - 1;
-}
-
-// One operand's requests of this lane: piece i of step s is read at p[i] +
-// s * advance while s * unit < lim[i], else from the page of zeros.
-template <int N>
-struct Requests {
-  const char *p[N];
-  int32_t lim[N];
-};
 
 // One output tile (the same in every lane).
 struct Tile {
@@ -135,257 +132,404 @@ struct Tile {
   int steps;
 };
 
-template <int KIND, int TYPE, int OUT, int BT, bool SWIGLU>
-__global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
+template <int KIND, int TYPE, int OUT, int CT, int STAGES, bool SWIGLU>
+__global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
+  constexpr int NT = 2 * CT, NW = NT / 64;  // CT / 64 x 2 waves of 64 x 64 results
+  constexpr int BT = kGrRows;
   constexpr bool MX = KIND == kGroupedMx, DW = KIND == kGroupedDw;
   constexpr bool ACROSS_A = KIND == kGroupedDx || DW, ACROSS_B = DW;  // reduction across the operand's rows
-  constexpr int NA = 4, NB = BT / 32;  // 1 KB requests a wave, a step
-  constexpr int FB = BT / 32;          // 16-row fragments of a wave along b
-  constexpr int kCols = SWIGLU ? kGrCols / 2 : kGrCols;
-  constexpr uint32_t kDataA = kGrCols * kGrStep, kDataB = BT * kGrStep;
-  constexpr uint32_t kScale = MX ? (kGrCols + BT) * 8 : 0;
-  constexpr uint32_t kBuf = kDataA + kDataB + kScale;
+  constexpr int NA = CT / 8 / NW, NB = BT / 8 / NW;                   // 1 KB requests a wave, a step
+  constexpr int FB = BT / 32;                                         // 16-row fragments of a wave along b
+  constexpr int kAhead = STAGES - 1;                                  // steps requested before they are multiplied
+  constexpr int kCols = SWIGLU ? CT / 2 : CT;
+  constexpr uint32_t kDataA = CT * kGrStep, kDataB = BT * kGrStep;
+  constexpr uint32_t kBuf = kDataA + kDataB;
+  constexpr uint32_t kScales = (CT + BT) * 16;  // MXFP4: 16 scale bytes a row, two steps' worth
   // The matrices' rows behind a lane's accumulators: fragments f and f + 1
   // interleaved in fours where that makes eight neighbouring 16-bit columns
   // a lane, else fragment by fragment.
-  constexpr bool kPairs = OUT != MOE_T_F32 && !ACROSS_A;
-  constexpr int kWords = OUT == MOE_T_F32 || kPairs ? 4 : 2;
+  constexpr bool kPairs = OUT != MOE_T_F32;
   constexpr int kChunks = (SWIGLU ? 2 : 4) / (kPairs ? 2 : 1);  // stores of a lane a row fragment
-  using Out = Packed<OUT, kWords>;
-  static_assert(!DW || BT == kGrCols, "dw tiles are square");
-  __shared__ __align__(1024) char lds[2 * kBuf];
-  __shared__ float row_scale[2][BT];
+  using Out = Packed<OUT, 4>;
+  // rows of an operand across the reduction in one request of a wave
+  constexpr int kRowsA = 1024 / (2 * CT), kRowsB = 1024 / (2 * BT);
   constexpr int kTokens = DW ? kGrRed : BT;
-  __shared__ int row_token[2][kTokens];
-  __shared__ int lo[kGrMaxExperts + 1], pre[DW ? 1 : kGrMaxExperts + 1];
-  __shared__ int scratch[kGrThreads / 64];
+  __shared__ __align__(1024) char lds[STAGES * kBuf];
+  __shared__ __align__(1024) char scales[MX ? STAGES * kScales : 16];
+  __shared__ int4 table[2 * kTableTiles];
+  __shared__ float row_scale[STAGES][BT];
+  __shared__ int row_token[STAGES][kTokens];
+  __shared__ int scratch[NW];
+  extern __shared__ int lo[];
+  int *pre = lo + a.E + 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wa = wave & 1, wb = wave >> 1;
+  const int wa = wave % (CT / 64), wb = wave / (CT / 64);
   const int l16 = lane & 15, g = lane >> 4;
   const char *zero = reinterpret_cast<const char *>(&g_zero_page);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const uint32_t scales0 = __builtin_amdgcn_readfirstlane(lds_addr(scales));
   const uint32_t token0 = __builtin_amdgcn_readfirstlane(lds_addr(row_token));
   const uint32_t scale0 = __builtin_amdgcn_readfirstlane(lds_addr(row_scale));
 
-  group_table<DW ? 0 : BT>(a, lo, pre, scratch);
-  const int n_items = DW ? a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[DW ? 0 : a.E]) * col_tiles;
-  // blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items
+  group_table<!DW, NT>(a, lo, pre, scratch);
+  const int n_items = DW ? a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[a.E]) * col_tiles;
+  // Blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items,
+  // its blocks in turn.  (Ranges of their own for 16, 8, 4 or 1 of the blocks
+  // lose the sharing in the L2: dw 606 -> 796, 784, 841, 1110 us.)
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
   const int end = static_cast<int>(static_cast<int64_t>(n_items) * (xcd + 1) / 8);
   const int begin = static_cast<int>(static_cast<int64_t>(n_items) * xcd / 8) + (blockIdx.x >> 3);
+  const int count = begin < end ? (end - begin + per - 1) / per : 0;  // this block's tiles
 
-  auto locate = [&](int item) __attribute__((always_inline)) {
+  // Places of tiles 32 c .. 32 c + 31 into the table's half c & 1: every
+  // expert's thread finds which of them are its.
+  auto fill_table = [&](int c) __attribute__((always_inline)) {
+    const int from = begin + c * kTableTiles * per;  // item of the first
+    for (int e = tid; e < a.E; e += NT) {
+      const int p0 = pre[e], p1 = pre[e + 1];
+      if (p1 <= p0) continue;
+      const int ahead = max(p0 * col_tiles - from, 0);
+      for (int i = (ahead + per - 1) / per; i < kTableTiles; ++i) {
+        const int item = from + i * per;
+        if (item >= p1 * col_tiles || item >= end) break;
+        const int j = item / col_tiles;
+        table[(c & 1) * kTableTiles + i] =
+            make_int4(e | (item - j * col_tiles) << 10, j - p0, lo[e], max(lo[e + 1] - lo[e], 0));
+      }
+    }
+  };
+  auto locate = [&](int i) __attribute__((always_inline)) {
     Tile t;
     if constexpr (DW) {
+      const int item = begin + i * per;
       t.e = item / (col_tiles * dw_tiles);
       const int in = item - t.e * (col_tiles * dw_tiles);
       t.bt = in / col_tiles;
       t.ct = in - t.bt * col_tiles;
+      t.r0 = __builtin_amdgcn_readfirstlane(lo[t.e]);
+      t.n = max(__builtin_amdgcn_readfirstlane(lo[t.e + 1]) - t.r0, 0);
     } else {
-      t.e = __builtin_amdgcn_readfirstlane(tile_expert(pre, a.E, item / col_tiles));
-      const int j = item / col_tiles;
-      t.ct = item - j * col_tiles;
-      t.bt = j - __builtin_amdgcn_readfirstlane(pre[t.e]);
+      const int4 v = table[i & (2 * kTableTiles - 1)];
+      const int ec = __builtin_amdgcn_readfirstlane(v.x);
+      t.e = ec & 1023;
+      t.ct = ec >> 10;
+      t.bt = __builtin_amdgcn_readfirstlane(v.y);
+      t.r0 = __builtin_amdgcn_readfirstlane(v.z);
+      t.n = __builtin_amdgcn_readfirstlane(v.w);
     }
-    t.r0 = __builtin_amdgcn_readfirstlane(lo[t.e]);
-    t.n = max(__builtin_amdgcn_readfirstlane(lo[t.e + 1]) - t.r0, 0);
     t.b_rows = (DW ? a.nb : t.n) - t.bt * BT;
     const int red = DW ? t.n : a.red;
     constexpr int kUnit = ACROSS_A ? kGrRed : kGrStep;
     t.steps = (red + kUnit - 1) / kUnit;
-    if (!DW && (t.bt < 0 || t.b_rows <= 0)) t.steps = 0;  // only where offsets overlap
     return t;
   };
-  // ---- The requesting side runs one step ahead of the products, across the
-  // tiles: while a tile's last step is multiplied and its results are
-  // stored, the next tile's first step is on its way.  The tokens of the
-  // rows that a request gathers are brought to LDS a step earlier still; they
-  // never pass through registers on the way, where the compiler would wait
-  // for them (and so for all requests before them).
-  int next = begin;  // item of the next request
-  int next_step = 0;
-  int tiles_begun = 0;
-  int slot = 0;  // of row_token: the next request's tokens
-  Tile nt{};
-  Requests<NA> ra;
-  Requests<NB> rb;
-  const char *sp[2] = {zero, zero};
-  int slim[2] = {INT32_MIN, INT32_MIN};
+
+  // ---- The requesting side runs kAhead steps before the products, across
+  // the tiles: while a tile's last steps are multiplied and its results are
+  // stored, the next tile's first are on their way.  The tokens of the rows
+  // that a request gathers are brought to LDS as many steps earlier still;
+  // they never pass through registers on the way, where the compiler would
+  // wait for them (and so for all requests before them).
+  struct Cursor {
+    Tile t;
+    int i, step, slot;  // tile of this block, its step, index modulo STAGES
+  };
+  auto settle = [&](Cursor &c) __attribute__((always_inline)) {  // on a tile with steps, or past the last
+    while (c.i < count) {
+      c.t = locate(c.i);
+      if (!DW || c.t.steps > 0) break;
+      ++c.i;
+    }
+  };
+  auto advance = [&](Cursor &c) __attribute__((always_inline)) {
+    c.slot = c.slot == kAhead ? 0 : c.slot + 1;
+    if (++c.step < c.t.steps) return;
+    c.step = 0;
+    ++c.i;
+    settle(c);
+  };
   const bool gather = KIND != kGroupedDx && a.row_tok;
+  Cursor tok{}, req{};
+  // Requests of this lane.  An operand whose rows follow one another is read
+  // at a base that is the same in every lane (moved on by `..._next` a step)
+  // plus off[i]; gathered rows at p[i], moved on by move[i].  Rows and columns
+  // past the operand's end read its last: their results are not stored.  What
+  // lies past the end of the reduction (in a tile's last step only) and rows
+  // of tokens out of range read the page of zeros.
+  const char *a_base[2], *b_base = nullptr;
+  uint32_t a_off[NA], b_off[NB];
+  const char *b_p[NB];
+  uint32_t b_move[NB];
+  int scale_fill = 0;  // of `scales`: where the next two steps' go
+  const int64_t a_next = ACROSS_A ? kGrRed * a.a_ld : kGrStep, b_next = kGrRed * a.b_ld;
+  int scale_slot = 0;
 
   auto request_tokens = [&]() __attribute__((always_inline)) {
-    if (!gather || (!DW && next_step > 0)) return;
-    slot ^= 1;
-    if (64 * wave < kTokens) {
-      const int r = (DW ? next_step * kGrRed : nt.bt * BT) + 64 * wave + lane;
-      direct4(reinterpret_cast<const char *>(a.row_tok + nt.r0 + (r < nt.n ? r : 0)),
-              token0 + (slot * kTokens + 64 * wave) * 4);
+    if (!gather || tok.i >= count) return;
+    if ((DW || tok.step == 0) && 64 * wave < kTokens) {
+      const int r = (DW ? tok.step * kGrRed : tok.t.bt * BT) + 64 * wave + lane;
+      direct4(r < tok.t.n ? reinterpret_cast<const char *>(a.row_tok + tok.t.r0 + r) : zero,
+              token0 + (tok.slot * kTokens + 64 * wave) * 4);
     }
+    advance(tok);
   };
   // row of the gathered operand behind row r of the group, `at` of the
-  // request's; -1: none
+  // request's; -1: zeros
   auto source = [&](int r, int at) __attribute__((always_inline)) {
-    if (r >= nt.n) return -1;
-    if (!gather) return nt.r0 + r;
-    const int k = row_token[slot][at];
+    if (!gather) return req.t.r0 + max(min(r, req.t.n - 1), 0);
+    const int k = row_token[req.slot][at];
     return static_cast<uint32_t>(k) < static_cast<uint32_t>(a.T) ? k : -1;
   };
-  auto find_next = [&]() __attribute__((always_inline)) {
-    while (next < end) {
-      nt = locate(next);
-      if (nt.steps > 0) break;
-      next += per;
-    }
-    if (next < end) request_tokens();
+  // where this lane's requests lie in a tile: staged row and its piece
+  auto a_row = [&](int i) __attribute__((always_inline)) {
+    return ACROSS_A ? kRowsA * (wave + NW * i) + lane / (64 / kRowsA) : 8 * (wave + NW * i) + (lane >> 3);
   };
-  // addresses of tile nt's requests
+  auto a_piece = [&](int i) __attribute__((always_inline)) {
+    const int R = a_row(i);
+    return ACROSS_A ? (lane % (64 / kRowsA)) ^ swz_t(R) : (lane & 7) ^ swz<kPairs>(R);
+  };
+  auto b_row = [&](int i) __attribute__((always_inline)) {
+    return ACROSS_B ? kRowsB * (wave + NW * i) + g : 8 * (wave + NW * i) + (lane >> 3);
+  };
+  auto b_piece = [&](int i) __attribute__((always_inline)) {
+    const int R = b_row(i);
+    return ACROSS_B ? l16 ^ swz_t(R) : (lane & 7) ^ swz<false>(R);
+  };
+  // addresses of the tile's first requests
   auto set_up = [&]() __attribute__((always_inline)) {
-    const int c0 = nt.ct * kCols, b0 = nt.bt * BT;
-    const int red = DW ? nt.n : a.red;
-    const char *abase = a.a + static_cast<int64_t>(nt.e) * a.a_expert;
-    const char *upbase = SWIGLU ? a.a2 + static_cast<int64_t>(nt.e) * a.a_expert : nullptr;
+    const Tile &t = req.t;
+    const int c0 = t.ct * kCols, b0 = t.bt * BT;
+    if constexpr (DW) {
+      a_base[0] = a.a + (gather ? 0 : t.r0 * a.a_ld);
+      b_base = a.b + t.r0 * a.b_ld;
+#pragma unroll
+      for (int i = 0; i < NA; ++i) a_off[i] = 2 * min(c0 + 8 * a_piece(i), a.na - 8);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        b_off[i] = b_row(i) * static_cast<uint32_t>(a.b_ld) + 2 * min(b0 + 8 * b_piece(i), a.nb - 8);
+      return;
+    }
+    a_base[0] = a.a + t.e * a.a_expert + (ACROSS_A ? 0 : c0 * a.a_ld);
+    if constexpr (SWIGLU) a_base[1] = a.a2 + t.e * a.a_expert + c0 * a.a_ld;
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
+      const int R = a_row(i);
       if constexpr (ACROSS_A) {
-        const int R = 4 * (wave + 4 * i) + g;
-        const int col = c0 + 8 * (l16 ^ swz_t(R));
-        const bool ok = col < a.na;
-        // dw: the row is added a step at a time
-        ra.p[i] = (DW ? a.a : abase + R * a.a_ld) + 2 * static_cast<int64_t>(ok ? col : 0);
-        ra.lim[i] = ok ? red - R : INT32_MIN;
+        a_off[i] = R * static_cast<uint32_t>(a.a_ld) + 2 * min(c0 + 8 * a_piece(i), a.na - 8);
       } else {
-        const int R = 8 * (wave + 4 * i) + (lane >> 3);
-        const int piece = (lane & 7) ^ swz<kPairs>(R);
-        // SwiGLU: 32 gate rows, then their 32 up rows, for each half of the tile
-        const int col = SWIGLU ? c0 + 32 * (R >> 6) + (R & 31) : c0 + R;
-        const char *base = SWIGLU && (R & 32) ? upbase : abase;
-        const bool ok = col < a.na;
-        ra.p[i] = base + (ok ? col : 0) * a.a_ld + 16 * piece;
-        ra.lim[i] = ok ? red - 16 * piece : INT32_MIN;
+        // SwiGLU: 32 gate rows, then their 32 up rows, for each 64 of the tile
+        const int col = SWIGLU ? 32 * (R >> 6) + (R & 31) : R;
+        a_off[i] = min(col, a.na - 1 - c0) * static_cast<uint32_t>(a.a_ld) + 16 * a_piece(i);
       }
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      if constexpr (ACROSS_B) {
-        const int R = 4 * (wave + 4 * i) + g;
-        const int col = b0 + 8 * (l16 ^ swz_t(R));
-        const bool ok = col < a.nb;
-        rb.p[i] = a.b + (nt.r0 + static_cast<int64_t>(R)) * a.b_ld + 2 * static_cast<int64_t>(ok ? col : 0);
-        rb.lim[i] = ok ? red - R : INT32_MIN;
-      } else {
-        const int R = 8 * (wave + 4 * i) + (lane >> 3);
-        const int piece = (lane & 7) ^ swz<false>(R);
-        const int src = source(b0 + R, R);
-        rb.p[i] = a.b + max(src, 0) * a.b_ld + 16 * piece;
-        rb.lim[i] = src >= 0 ? (KIND == kGroupedDx ? 2 * red : red) - 16 * piece : INT32_MIN;
-      }
-    }
-    // MXFP4: eight scale bytes a row and step, two 4-byte requests a lane,
-    // each request of a wave 32 rows of a or b
-    if constexpr (MX) {
-      const int j = 4 * (lane & 1);
-      const int R = 32 * wave + (lane >> 1);
-      const int col = SWIGLU ? c0 + 32 * (R >> 6) + (R & 31) : c0 + R;
-      const char *base = SWIGLU && (R & 32) ? a.as2 : a.as;
-      sp[0] = base + (static_cast<int64_t>(nt.e) * a.na + (col < a.na ? col : 0)) * a.s_ld + j;
-      slim[0] = col < a.na ? a.s_ld - j : INT32_MIN;
-      const int src = R < BT ? source(b0 + R, R) : -1;
-      sp[1] = a.bs + static_cast<int64_t>(max(src, 0)) * a.s_ld + j;
-      slim[1] = src >= 0 ? a.s_ld - j : INT32_MIN;
+      const int src = source(b0 + b_row(i), b_row(i));
+      b_p[i] = src < 0 ? zero : a.b + src * a.b_ld + 16 * b_piece(i);
+      b_move[i] = src < 0 ? 0 : kGrStep;
     }
   };
-  // requests the next step into buffer `b`
+  // MXFP4: the scales of steps 2 c and 2 c + 1 of every staged row (SwiGLU:
+  // staged rows are 32 gate rows, then their 32 up rows, for each 64), 16
+  // bytes a row and a lane: a request touches a cache line a row whatever it
+  // takes from it, so fewer and larger ones (8 bytes a step: MXFP4 down of
+  // 131072 rows 240 us, gate/up of 16384 rows 83 us).
+  const char *scale_row = nullptr;  // of staged row 64 wave + lane (a's rows, then b's), at the tile's begin
+  auto request_scales = [&]() __attribute__((always_inline)) {
+    if (64 * wave >= CT + BT) return;
+    const Tile &t = req.t;
+    if (req.step == 0) {
+      const int R = 64 * wave + lane;
+      if (R < CT) {
+        const int c0 = t.ct * kCols;
+        const int col = SWIGLU ? 32 * (R >> 6) + (R & 31) : R;
+        scale_row = (SWIGLU && (R & 32) ? a.as2 : a.as) +
+                    (static_cast<int64_t>(t.e) * a.na + c0 + min(col, a.na - 1 - c0)) * a.s_ld;
+      } else {
+        const int src = source(t.bt * BT + R - CT, R - CT);
+        scale_row = src < 0 ? nullptr : a.bs + static_cast<int64_t>(src) * a.s_ld;
+      }
+    }
+    const int c = 8 * req.step;  // first scale byte
+    const uint32_t dst = scales0 + scale_fill * kScales + 1024 * wave;
+    if (a.s_ld % 16 == 0) {
+      direct16(scale_row ? scale_row + c : zero, dst);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // word by word; none past the row's end
+        const int from = 16 * i + (lane >> 2);
+        const uint64_t row = reinterpret_cast<uint64_t>(scale_row);
+        const uint64_t lo32 = static_cast<uint32_t>(__shfl(static_cast<int>(row), from));
+        const uint64_t hi32 = static_cast<uint32_t>(__shfl(static_cast<int>(row >> 32), from));
+        const char *p = reinterpret_cast<const char *>(hi32 << 32 | lo32);
+        const int at = c + 4 * (lane & 3);
+        direct4(p && at < a.s_ld ? p + at : zero, dst + 256 * i);
+      }
+    }
+    scale_fill = scale_fill == kAhead ? 0 : scale_fill + 1;
+  };
+  // requests the next step into buffer `b`: at least kRequests operations
+  constexpr int kRequests = NA + NB;
   auto issue = [&](int b) __attribute__((always_inline)) {
-    if (next >= end) return;
-    const int s = next_step;
+    request_tokens();
     const uint32_t buf = lds0 + b * kBuf;
-    if (s == 0) {
+    if (req.step == 0) {
       set_up();
       if (!DW && a.row_w && 64 * wave < BT) {
-        const int r = 64 * wave + lane;
-        direct4(r < nt.b_rows ? reinterpret_cast<const char *>(a.row_w + nt.r0 + nt.bt * BT + r) : zero,
-                scale0 + ((tiles_begun & 1) * BT + 64 * wave) * 4);
+        const int r = req.t.bt * BT + 64 * wave + lane;
+        direct4(reinterpret_cast<const char *>(a.row_w + req.t.r0 + max(min(r, req.t.n - 1), 0)),
+                scale0 + (scale_slot * BT + 64 * wave) * 4);
       }
-      ++tiles_begun;
-    }
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const char *p;
-      if constexpr (DW) {
-        const int at = 4 * (wave + 4 * i) + g;
-        const int src = source(s * kGrRed + at, at);
-        p = ra.lim[i] > s * kGrRed && src >= 0 ? ra.p[i] + src * a.a_ld : zero;
-      } else if constexpr (ACROSS_A)
-        p = ra.lim[i] > s * kGrRed ? ra.p[i] + s * (kGrRed * a.a_ld) : zero;
-      else
-        p = ra.lim[i] > s * kGrStep ? ra.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
-      direct16(p, buf + 1024 * (wave + 4 * i));
-    }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const char *p;
-      if constexpr (ACROSS_B)
-        p = rb.lim[i] > s * kGrRed ? rb.p[i] + s * (kGrRed * a.b_ld) : zero;
-      else
-        p = rb.lim[i] > s * kGrStep ? rb.p[i] + s * static_cast<int64_t>(kGrStep) : zero;
-      direct16(p, buf + kDataA + 1024 * (wave + 4 * i));
+      scale_slot = scale_slot == kAhead ? 0 : scale_slot + 1;
     }
     if constexpr (MX) {
-      direct4(slim[0] > 8 * s ? sp[0] + 8 * s : zero, buf + kDataA + kDataB + 256 * wave);
-      if (32 * wave < BT)
-        direct4(slim[1] > 8 * s ? sp[1] + 8 * s : zero, buf + kDataA + kDataB + kGrCols * 8 + 256 * wave);
+      if ((req.step & 1) == 0) request_scales();
     }
-    if (++next_step == nt.steps) {
-      next_step = 0;
-      next += per;
-      find_next();
+    // what is left of the reduction: bytes of a row, or rows
+    const int left = (DW ? req.t.n : a.red) - req.step * (ACROSS_A ? kGrRed : kGrStep);
+    const uint32_t at_a = buf + 1024 * wave, at_b = at_a + kDataA;
+    auto a_from = [&](int i) __attribute__((always_inline)) { return a_base[SWIGLU ? (a_row(i) >> 5) & 1 : 0]; };
+    if (left >= (ACROSS_A ? kGrRed : kGrStep)) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const uint32_t dst = at_a + 1024 * NW * i;
+        if (DW && gather) {
+          const int src = source(0, a_row(i));
+          direct16(src < 0 ? zero : a_base[0] + src * a.a_ld + a_off[i], dst);
+        } else if constexpr (DW) {
+          direct16(a_base[0], a_row(i) * static_cast<uint32_t>(a.a_ld) + a_off[i], dst);
+        } else {
+          direct16(a_from(i), a_off[i], dst);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t dst = at_b + 1024 * NW * i;
+        if constexpr (ACROSS_B)
+          direct16(b_base, b_off[i], dst);
+        else
+          direct16(b_p[i], dst);
+      }
     } else {
-      request_tokens();
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const char *p;
+        if (DW && gather) {
+          const int src = source(0, a_row(i));
+          p = src < 0 || a_row(i) >= left ? zero : a_base[0] + src * a.a_ld + a_off[i];
+        } else if constexpr (DW) {
+          p = a_row(i) < left ? a_base[0] + (a_row(i) * static_cast<uint32_t>(a.a_ld) + a_off[i]) : zero;
+        } else {
+          p = (ACROSS_A ? a_row(i) : 16 * a_piece(i)) < left ? a_from(i) + a_off[i] : zero;
+        }
+        direct16(p, at_a + 1024 * NW * i);
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const char *p;
+        if constexpr (ACROSS_B)
+          p = b_row(i) < left ? b_base + b_off[i] : zero;
+        else
+          p = 16 * b_piece(i) < (KIND == kGroupedDx ? 2 * left : left) ? b_p[i] : zero;
+        direct16(p, at_b + 1024 * NW * i);
+      }
     }
+    a_base[0] += DW && gather ? 0 : a_next;
+    if constexpr (SWIGLU) a_base[1] += a_next;
+    if constexpr (ACROSS_B) {
+      b_base += b_next;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) b_p[i] += b_move[i];
+    }
+    advance(req);
   };
 
-  find_next();
+  if constexpr (!DW) {
+    fill_table(0);
+    lds_barrier();
+  }
+  settle(req);
+  settle(tok);
+  for (int k = 0; k < kAhead; ++k) request_tokens();
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-  lds_barrier();
-  issue(0);
-  int buf = 0;
-  int tiles_done = 0;
-  bool younger = false;  // the tile's first requests were followed by a whole tile's stores
-  for (int item = begin; item < end; item += per) {
-    const Tile t = locate(item);
+
+  // Steps requested and not yet multiplied are counted by the vector memory
+  // operations surely made after their requests: operations complete in the
+  // order they were made, so waiting until no more than those are left waits
+  // for the requests, and not for later ones or for a tile's stores.
+  constexpr int kStores = FB * kChunks;  // of a whole tile
+  int after[kAhead] = {};
+  int buf = 0, fill = 0;  // buffers of the next step multiplied and requested
+  auto request = [&]() __attribute__((always_inline)) {
+    if (req.i >= count) return;
+    issue(fill);
+    fill = fill == kAhead ? 0 : fill + 1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) after[k] += kRequests;
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    lds_barrier();
+    request();
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m)
+      if (m >= k) after[m] = 0;
+  }
+  int done_slot = 0;   // of row_scale
+  int scale_read = 0;  // of `scales`
+  for (int i = 0; i < count; ++i) {
+    if constexpr (!DW) {
+      // the next half of the table, once every wave has left the one it takes
+      if ((i & (kTableTiles - 1)) == 0) {
+        lds_barrier();
+        fill_table(i / kTableTiles + 1);
+        lds_barrier();
+      }
+    }
+    const Tile t = locate(i);
     f32x4_t acc[4][FB];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int h = 0; h < FB; ++h) acc[f][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
     for (int s = 0; s < t.steps; ++s) {
-      // this step's requests have landed; requests and stores are counted in
-      // the order they were made, so the stores behind them may be under way
-      if (s == 0 && younger)
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(FB * kChunks));
+      if (after[0] >= kRequests + kStores)
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(kRequests + kStores));
+      else if (after[0] >= (kRequests > kStores ? kRequests : kStores))
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kRequests > kStores ? kRequests : kStores)));
+      else if (after[0] >= (kRequests < kStores ? kRequests : kStores))
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kRequests < kStores ? kRequests : kStores)));
       else
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-      lds_barrier();
-      if (next < end) issue(buf ^ 1);
+      lds_barrier();  // every wave's part has landed, and the buffer before is free
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) after[k] = after[k + 1];
+      after[kAhead - 1] = -kRequests;
       const char *ta = lds + buf * kBuf;
       const char *tb = ta + kDataA;
-      const char *ts = tb + kDataB;
-      buf ^= 1;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      const char *ts = scales + scale_read * kScales + 8 * (s & 1);
+      if ((s & 1) || s + 1 == t.steps) scale_read = scale_read == kAhead ? 0 : scale_read + 1;
+      buf = buf == kAhead ? 0 : buf + 1;
+      u32x4_t A[4], B[FB];
+      uint32_t sa[4] = {}, sb[FB] = {};
+      auto read = [&](int kk) __attribute__((always_inline)) {
         auto along = [&](const char *t, int R, int sw) __attribute__((always_inline)) {
           const uint4 v = *reinterpret_cast<const uint4 *>(t + R * kGrStep + 16 * ((4 * kk + g) ^ sw));
           return u32x4_t{v.x, v.y, v.z, v.w};
         };
-        // columns col .. col + 15 of staged rows 32 kk + 8 g .. + 7
-        auto across = [&](const char *t, int col) __attribute__((always_inline)) {
+        // a fragment of columns from `col` on, of staged rows 32 kk + 8 g ..
+        // + 7: 16 lanes give four rows' chunks of four columns, the chunk c =
+        // 0..3 of a row at columns 4 c, or (pair >= 0) 8 c + 4 pair
+        auto across = [&](const char *t, int row_bytes, int col, int pair) __attribute__((always_inline)) {
           u32x4_t r;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int R = 32 * kk + 8 * g + 4 * j + (l16 >> 2);
-            const int piece = (col / 8 + ((l16 >> 1) & 1)) ^ swz_t(R);
-            const char *p = t + R * 256 + 16 * piece + 8 * (l16 & 1);
+            const int piece = (col / 8 + (pair < 0 ? (l16 >> 1) & 1 : l16 & 3)) ^ swz_t(R);
+            const char *p = t + R * row_bytes + 16 * piece + 8 * (pair < 0 ? l16 & 1 : pair);
             const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4_t *)(const_cast<char *>(p)));
             const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
@@ -394,28 +538,28 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
           }
           return r;
         };
-        u32x4_t A[4], B[FB];
-        uint32_t sa[4] = {}, sb[FB] = {};
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           if constexpr (ACROSS_A) {
-            A[f] = across(ta, 64 * wa + 16 * f);
+            A[f] = kPairs ? across(ta, 2 * CT, 64 * wa + 32 * (f >> 1), f & 1) : across(ta, 2 * CT, 64 * wa + 16 * f, -1);
           } else {
             const int R = 64 * wa + (kPairs ? 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3) : 16 * f + l16);
             A[f] = along(ta, R, swz<kPairs>(R));
-            if constexpr (MX) sa[f] = *reinterpret_cast<const uint32_t *>(ts + 8 * R + 4 * kk) >> (8 * g);
+            if constexpr (MX) sa[f] = *reinterpret_cast<const uint32_t *>(ts + 16 * R + 4 * kk) >> (8 * g);
           }
         }
 #pragma unroll
         for (int h = 0; h < FB; ++h) {
           const int R = wb * (BT / 2) + 16 * h + l16;
           if constexpr (ACROSS_B) {
-            B[h] = across(tb, wb * (BT / 2) + 16 * h);
+            B[h] = across(tb, 2 * BT, wb * (BT / 2) + 16 * h, -1);
           } else {
             B[h] = along(tb, R, swz<false>(R));
-            if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 8 * (kGrCols + R) + 4 * kk) >> (8 * g);
+            if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 16 * (CT + R) + 4 * kk) >> (8 * g);
           }
         }
+      };
+      auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -425,11 +569,16 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
             else
               acc[f][h] = mfma16<TYPE>(A[f], B[h], acc[f][h]);
           }
-      }
+      };
+      read(0);  // on their way while the next step is requested
+      request();
+      multiply();
+      read(1);
+      multiply();
     }
-    if (!DW && t.steps == 0) continue;
 
-    const float *scale = row_scale[tiles_done++ & 1];
+    const float *scale = row_scale[done_slot];
+    done_slot = done_slot == kAhead ? 0 : done_slot + 1;
     auto store_tile = [&](auto whole_t) __attribute__((always_inline)) {
       constexpr bool WHOLE = decltype(whole_t)::value != 0;
 #pragma unroll
@@ -447,7 +596,7 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
           for (int i = 0; i < Out::kCols; ++i) {
             const int f = kPairs ? 2 * c + (i >> 2) : c;
             v[i] = acc[f][h][i & 3];
-            if constexpr (SWIGLU) v[i] = v[i] / (1.f + expf(-v[i])) * acc[f + 2][h][i & 3];
+            if constexpr (SWIGLU) v[i] = swiglu(v[i], acc[f + 2][h][i & 3]);
             v[i] *= w;
           }
           Out o;
@@ -458,48 +607,73 @@ __global__ void __launch_bounds__(kGrThreads, 2) grouped_tile_kernel(GroupedArgs
         }
       }
     };
-    younger = a.out_vec && t.b_rows >= BT && (t.ct + 1) * kCols <= a.na;
-    if (younger)
+    if (a.out_vec && t.b_rows >= BT && (t.ct + 1) * kCols <= a.na) {
       store_tile(IntC<1>{});
-    else
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) after[k] += kStores;
+    } else {
       store_tile(IntC<0>{});
+    }
   }
 }
 
-template <int KIND, int TYPE, int OUT, int BT, bool SWIGLU = false>
+// Column tiles, and tiles at most (host: the kernel counts them itself).
+struct TileCount {
+  int32_t col_tiles, dw_tiles;
+  int64_t tiles;
+  TileCount(const GroupedArgs &a, int32_t cols) {
+    col_tiles = (a.na + cols - 1) / cols;
+    dw_tiles = (a.nb + kGrRows - 1) / kGrRows;
+    const int64_t rows = a.kind == kGroupedDw ? static_cast<int64_t>(a.E) * dw_tiles
+                                              : a.n_rows / kGrRows + static_cast<int64_t>(a.E < a.n_rows ? a.E : a.n_rows);
+    tiles = rows * col_tiles;
+  }
+};
+
+template <int KIND, int TYPE, int OUT, int CT, int STAGES, bool SWIGLU>
 hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
-  const int32_t cols = SWIGLU ? kGrCols / 2 : kGrCols;
-  const int32_t col_tiles = (a.na + cols - 1) / cols;
-  const int32_t dw_tiles = (a.nb + kGrCols - 1) / kGrCols;
-  // items at most (host): the kernel counts them itself
-  const int64_t tiles = KIND == kGroupedDw ? static_cast<int64_t>(a.E) * dw_tiles
-                                           : a.n_rows / BT + static_cast<int64_t>(a.E < a.n_rows ? a.E : a.n_rows);
-  const int64_t items = tiles * col_tiles;
-  const int64_t blocks = (items + 7) / 8 * 8;
-  constexpr int64_t kMost = 512;  // two blocks a compute unit
-  grouped_tile_kernel<KIND, TYPE, OUT, BT, SWIGLU>
-      <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), kGrThreads, 0, s>>>(a, col_tiles, dw_tiles);
+  const TileCount n(a, SWIGLU ? CT / 2 : CT);
+  constexpr int64_t kMost = CT == 128 ? 512 : 256;  // blocks that the compute units hold
+  const int64_t blocks = (n.tiles + 7) / 8 * 8;
+  const uint32_t lds = (a.E + 1) * sizeof(int) * (KIND == kGroupedDw ? 1 : 2);
+  grouped_tile_kernel<KIND, TYPE, OUT, CT, STAGES, SWIGLU>
+      <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), 2 * CT, lds, s>>>(a, n.col_tiles, n.dw_tiles);
   return hipGetLastError();
+}
+
+// 256 columns and three buffers, one block a compute unit, or 128 columns and
+// two buffers, two blocks.  The wide tile reads less for a result and runs
+// two steps ahead; the narrow one leaves fewer compute units idle.  From four
+// wide tiles a compute unit on the wide one wins: dw of 512 and 32768 rows
+// over 256 experts of 1024 x 2048 342 against 403 us and 520 against 602, fwd
+// of 32768 rows 275 against 297, dx 278 against 297; below it the narrow one:
+// 512 rows over eight experts of 2048 x 2048 fwd 29.0 against 34.7, dw of one
+// expert 106 against 139.  MXFP4's scales leave the wide tile no third buffer,
+// and with two it loses (gate/up of 16384 rows 91 against 80 us).
+template <int KIND, int TYPE, int OUT>
+hipError_t launch_width(const GroupedArgs &a, hipStream_t s) {
+  return TileCount(a, 256).tiles >= 1024 ? launch_tile<KIND, TYPE, OUT, 256, 3, false>(a, s)
+                                         : launch_tile<KIND, TYPE, OUT, 128, 2, false>(a, s);
 }
 
 template <int KIND>
 hipError_t launch_16bit(const GroupedArgs &a, hipStream_t s) {
   if (a.type == MOE_T_BF16)
-    return a.out_type == MOE_T_F32 ? launch_tile<KIND, MOE_T_BF16, MOE_T_F32, 128>(a, s)
-                                   : launch_tile<KIND, MOE_T_BF16, MOE_T_BF16, 128>(a, s);
-  return a.out_type == MOE_T_F32 ? launch_tile<KIND, MOE_T_F16, MOE_T_F32, 128>(a, s)
-                                 : launch_tile<KIND, MOE_T_F16, MOE_T_F16, 128>(a, s);
+    return a.out_type == MOE_T_F32 ? launch_width<KIND, MOE_T_BF16, MOE_T_F32>(a, s)
+                                   : launch_width<KIND, MOE_T_BF16, MOE_T_BF16>(a, s);
+  return a.out_type == MOE_T_F32 ? launch_width<KIND, MOE_T_F16, MOE_T_F32>(a, s)
+                                 : launch_width<KIND, MOE_T_F16, MOE_T_F16>(a, s);
 }
 
 template <bool SWIGLU>
 hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
   switch (a.out_type) {
     case MOE_T_BF16:
-      return launch_tile<kGroupedMx, 0, MOE_T_BF16, 128, SWIGLU>(a, s);
+      return launch_tile<kGroupedMx, 0, MOE_T_BF16, 128, 2, SWIGLU>(a, s);
     case MOE_T_F16:
-      return launch_tile<kGroupedMx, 0, MOE_T_F16, 128, SWIGLU>(a, s);
+      return launch_tile<kGroupedMx, 0, MOE_T_F16, 128, 2, SWIGLU>(a, s);
     default:
-      return launch_tile<kGroupedMx, 0, MOE_T_F32, 128, SWIGLU>(a, s);
+      return launch_tile<kGroupedMx, 0, MOE_T_F32, 128, 2, SWIGLU>(a, s);
   }
 }
 
@@ -512,10 +686,7 @@ hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
 // 29.8 against 32.4 us, MXFP4 12.0 against 20.0; 1024 rows of one matrix 17.0
 // against 34.3.
 bool few_rows(const GroupedArgs &a) {
-  if (a.kind != kGroupedFwd && a.kind != kGroupedMx) return false;
-  const int32_t cols = a.a2 ? kGrCols / 2 : kGrCols;
-  const int32_t tiles = a.n_rows / 128 + (a.E < a.n_rows ? a.E : a.n_rows);
-  return a.n_rows <= 256 && static_cast<int64_t>(tiles) * ((a.na + cols - 1) / cols) <= 256;
+  return (a.kind == kGroupedFwd || a.kind == kGroupedMx) && a.n_rows <= 256 && TileCount(a, a.a2 ? 64 : 128).tiles <= 256;
 }
 
 }  // namespace

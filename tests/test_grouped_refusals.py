@@ -95,6 +95,7 @@ def test_grouped_gemm_common_refusals(lib, name, base, kw, rc):
     ("moe_grouped_gemm", F, dict(x=P + 8), -1),
     ("moe_grouped_gemm", F, dict(x_ld=56), -1),
     ("moe_grouped_gemm", F, dict(x_ld=68), -2),
+    ("moe_grouped_gemm", F, dict(x_ld=2 ** 24 + 8), -2),
     ("moe_grouped_gemm", F, dict(out=P + 4), -1),
     ("moe_grouped_gemm", F, dict(out_ld=44), -2),
     ("moe_grouped_gemm", F, dict(row_w=P + 1), -1),
