@@ -95,33 +95,44 @@ MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
 // 0) rows.
 template <bool PRE, int NT>
 MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= a.E; e += NT)
-    lo[e] = a.offsets ? min(max(a.offsets[e], 0), a.n_rows) : e * a.n_rows;  // without offsets E is 1
-  lds_barrier();
-  if constexpr (PRE) {
-    constexpr int kPer = kGrMaxExperts / NT;
-    int cnt[kPer], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      cnt[i] = e < a.E ? (max(lo[e + 1] - lo[e], 0) + kGrRows - 1) / kGrRows : 0;
-      mine += cnt[i];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  int before = 0;  // row tiles of the experts of earlier passes
+  for (int e0 = 0; e0 <= a.E; e0 += NT) {
+    const int e = e0 + tid;
+    int first = 0, n = 0;
+    if (e <= a.E) {
+      // without offsets E is 1
+      first = a.offsets ? min(max(a.offsets[e], 0), a.n_rows) : e * a.n_rows;
+      if (e < a.E) n = max((a.offsets ? min(max(a.offsets[e + 1], 0), a.n_rows) : a.n_rows) - first, 0);
+      lo[e] = first;
     }
-    const int inc = wave_scan(mine);
-    if (lane == 63) scratch[wave] = inc;
-    lds_barrier();
-    int base = inc - mine;
-    for (int w = 0; w < wave; ++w) base += scratch[w];
+    if constexpr (PRE) {
+      const int mine = (n + kGrRows - 1) / kGrRows;
+      const int upto = wave_scan(mine);
+      if (e0 > 0) lds_barrier();  // scratch has been read
+      if (lane_id() == 63) scratch[wave] = upto;
+      lds_barrier();
+      int base = before, all = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      if (e <= a.E) pre[e] = base;
-      base += cnt[i];
+      for (int w = 0; w < NT / 64; ++w) {
+        const int x = scratch[w];
+        base += w < wave ? x : 0;
+        all += x;
+      }
+      if (e <= a.E) pre[e] = base + upto - mine;
+      before += all;
     }
-    if (tid == NT - 1 && a.E == kGrMaxExperts) pre[kGrMaxExperts] = base;
-    lds_barrier();
   }
+  lds_barrier();
+}
+
+// The expert of row tile j (pre[e] <= j < pre[e + 1]), found by the whole
+// wave: among every 16th entry, then among those 16.
+MOE_DEV int tile_expert(const int *pre, int E, int j) {
+  const int lane = lane_id();
+  const int c = __popcll(__ballot(16 * lane < E && pre[16 * lane] <= j)) - 1;
+  const int i = 16 * c + (lane & 15);
+  return 16 * c + __popcll(__ballot(lane < 16 && i < E && pre[i] <= j)) - 1;
 }
 
 // One output tile (the same in every lane).
@@ -182,21 +193,17 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
   const int begin = static_cast<int>(static_cast<int64_t>(n_items) * xcd / 8) + (blockIdx.x >> 3);
   const int count = begin < end ? (end - begin + per - 1) / per : 0;  // this block's tiles
 
-  // Places of tiles 32 c .. 32 c + 31 into the table's half c & 1: every
-  // expert's thread finds which of them are its.
+  // Places of tiles 32 c .. 32 c + 31 into the table's half c & 1, a wave a
+  // tile.
   auto fill_table = [&](int c) __attribute__((always_inline)) {
-    const int from = begin + c * kTableTiles * per;  // item of the first
-    for (int e = tid; e < a.E; e += NT) {
-      const int p0 = pre[e], p1 = pre[e + 1];
-      if (p1 <= p0) continue;
-      const int ahead = max(p0 * col_tiles - from, 0);
-      for (int i = (ahead + per - 1) / per; i < kTableTiles; ++i) {
-        const int item = from + i * per;
-        if (item >= p1 * col_tiles || item >= end) break;
-        const int j = item / col_tiles;
+    const int from = c * kTableTiles, n = min(count - from, kTableTiles);
+    for (int i = wave; i < n; i += NW) {
+      const int item = begin + (from + i) * per;
+      const int j = item / col_tiles;
+      const int e = tile_expert(pre, a.E, j);
+      if (lane == 0)
         table[(c & 1) * kTableTiles + i] =
-            make_int4(e | (item - j * col_tiles) << 10, j - p0, lo[e], max(lo[e + 1] - lo[e], 0));
-      }
+            make_int4(e | (item - j * col_tiles) << 10, j - pre[e], lo[e], max(lo[e + 1] - lo[e], 0));
     }
   };
   auto locate = [&](int i) __attribute__((always_inline)) {
@@ -451,9 +458,11 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
     lds_barrier();
   }
   settle(req);
-  settle(tok);
-  for (int k = 0; k < kAhead; ++k) request_tokens();
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  if (gather) {
+    tok = req;
+    for (int k = 0; k < kAhead; ++k) request_tokens();
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  }
 
   // Steps requested and not yet multiplied are counted by the vector memory
   // operations surely made after their requests: operations complete in the
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
   for (int i = 0; i < count; ++i) {
     if constexpr (!DW) {
       // the next half of the table, once every wave has left the one it takes
-      if ((i & (kTableTiles - 1)) == 0) {
+      if ((i & (kTableTiles - 1)) == 0 && i + kTableTiles < count) {
         lds_barrier();
         fill_table(i / kTableTiles + 1);
         lds_barrier();
@@ -495,6 +504,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
 #pragma unroll
       for (int h = 0; h < FB; ++h) acc[f][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+    const int fragments = (t.b_rows - wb * (BT / 2) + 15) >> 4;  // of this wave that have rows, or more than FB
     for (int s = 0; s < t.steps; ++s) {
       if (after[0] >= kRequests + kStores)
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(kRequests + kStores));
@@ -508,85 +518,100 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
 #pragma unroll
       for (int k = 0; k + 1 < kAhead; ++k) after[k] = after[k + 1];
       after[kAhead - 1] = -kRequests;
+      request();
       const char *ta = lds + buf * kBuf;
       const char *tb = ta + kDataA;
       const char *ts = scales + scale_read * kScales + 8 * (s & 1);
       if ((s & 1) || s + 1 == t.steps) scale_read = scale_read == kAhead ? 0 : scale_read + 1;
       buf = buf == kAhead ? 0 : buf + 1;
-      u32x4_t A[4], B[FB];
-      uint32_t sa[4] = {}, sb[FB] = {};
-      auto read = [&](int kk) __attribute__((always_inline)) {
-        auto along = [&](const char *t, int R, int sw) __attribute__((always_inline)) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(t + R * kGrStep + 16 * ((4 * kk + g) ^ sw));
-          return u32x4_t{v.x, v.y, v.z, v.w};
+      // the step's products of the first NF row fragments
+      auto step = [&](auto nf_t) __attribute__((always_inline)) {
+        constexpr int NF = decltype(nf_t)::value;
+        u32x4_t A[4], B[NF ? NF : 1];
+        uint32_t sa[4] = {}, sb[NF ? NF : 1] = {};
+        auto read = [&](int kk) __attribute__((always_inline)) {
+          if constexpr (NF == 0) return;
+          auto along = [&](const char *t, int R, int sw) __attribute__((always_inline)) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(t + R * kGrStep + 16 * ((4 * kk + g) ^ sw));
+            return u32x4_t{v.x, v.y, v.z, v.w};
+          };
+          // a fragment of columns from `col` on, of staged rows 32 kk + 8 g ..
+          // + 7: 16 lanes give four rows' chunks of four columns, the chunk c
+          // = 0..3 of a row at columns 4 c, or (pair >= 0) 8 c + 4 pair
+          auto across = [&](const char *t, int row_bytes, int col, int pair) __attribute__((always_inline)) {
+            u32x4_t r;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int R = 32 * kk + 8 * g + 4 * j + (l16 >> 2);
+              const int piece = (col / 8 + (pair < 0 ? (l16 >> 1) & 1 : l16 & 3)) ^ swz_t(R);
+              const char *p = t + R * row_bytes + 16 * piece + 8 * (pair < 0 ? l16 & 1 : pair);
+              const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (__attribute__((address_space(3))) s16x4_t *)(const_cast<char *>(p)));
+              const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
+              r[2 * j] = u.x;
+              r[2 * j + 1] = u.y;
+            }
+            return r;
+          };
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            if constexpr (ACROSS_A) {
+              A[f] = kPairs ? across(ta, 2 * CT, 64 * wa + 32 * (f >> 1), f & 1)
+                            : across(ta, 2 * CT, 64 * wa + 16 * f, -1);
+            } else {
+              const int R =
+                  64 * wa + (kPairs ? 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3) : 16 * f + l16);
+              A[f] = along(ta, R, swz<kPairs>(R));
+              if constexpr (MX) sa[f] = *reinterpret_cast<const uint32_t *>(ts + 16 * R + 4 * kk) >> (8 * g);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < NF; ++h) {
+            const int R = wb * (BT / 2) + 16 * h + l16;
+            if constexpr (ACROSS_B) {
+              B[h] = across(tb, 2 * BT, wb * (BT / 2) + 16 * h, -1);
+            } else {
+              B[h] = along(tb, R, swz<false>(R));
+              if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 16 * (CT + R) + 4 * kk) >> (8 * g);
+            }
+          }
         };
-        // a fragment of columns from `col` on, of staged rows 32 kk + 8 g ..
-        // + 7: 16 lanes give four rows' chunks of four columns, the chunk c =
-        // 0..3 of a row at columns 4 c, or (pair >= 0) 8 c + 4 pair
-        auto across = [&](const char *t, int row_bytes, int col, int pair) __attribute__((always_inline)) {
-          u32x4_t r;
+        auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int R = 32 * kk + 8 * g + 4 * j + (l16 >> 2);
-            const int piece = (col / 8 + (pair < 0 ? (l16 >> 1) & 1 : l16 & 3)) ^ swz_t(R);
-            const char *p = t + R * row_bytes + 16 * piece + 8 * (pair < 0 ? l16 & 1 : pair);
-            const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4_t *)(const_cast<char *>(p)));
-            const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
-            r[2 * j] = u.x;
-            r[2 * j + 1] = u.y;
-          }
-          return r;
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int h = 0; h < NF; ++h) {
+              if constexpr (MX)
+                acc[f][h] = mfma_mx(A[f], B[h], acc[f][h], sa[f], sb[h]);
+              else
+                acc[f][h] = mfma16<TYPE>(A[f], B[h], acc[f][h]);
+            }
         };
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          if constexpr (ACROSS_A) {
-            A[f] = kPairs ? across(ta, 2 * CT, 64 * wa + 32 * (f >> 1), f & 1) : across(ta, 2 * CT, 64 * wa + 16 * f, -1);
-          } else {
-            const int R = 64 * wa + (kPairs ? 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3) : 16 * f + l16);
-            A[f] = along(ta, R, swz<kPairs>(R));
-            if constexpr (MX) sa[f] = *reinterpret_cast<const uint32_t *>(ts + 16 * R + 4 * kk) >> (8 * g);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < FB; ++h) {
-          const int R = wb * (BT / 2) + 16 * h + l16;
-          if constexpr (ACROSS_B) {
-            B[h] = across(tb, 2 * BT, wb * (BT / 2) + 16 * h, -1);
-          } else {
-            B[h] = along(tb, R, swz<false>(R));
-            if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 16 * (CT + R) + 4 * kk) >> (8 * g);
-          }
-        }
+        read(0);
+        multiply();
+        read(1);
+        multiply();
       };
-      auto multiply = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-          for (int h = 0; h < FB; ++h) {
-            if constexpr (MX)
-              acc[f][h] = mfma_mx(A[f], B[h], acc[f][h], sa[f], sb[h]);
-            else
-              acc[f][h] = mfma16<TYPE>(A[f], B[h], acc[f][h]);
-          }
-      };
-      read(0);  // on their way while the next step is requested
-      request();
-      multiply();
-      read(1);
-      multiply();
+      if (fragments > 2)
+        step(IntC<4>{});
+      else if (fragments == 2)
+        step(IntC<2>{});
+      else if (fragments == 1)
+        step(IntC<1>{});
+      else
+        step(IntC<0>{});
     }
 
     const float *scale = row_scale[done_slot];
     done_slot = done_slot == kAhead ? 0 : done_slot + 1;
     auto store_tile = [&](auto whole_t) __attribute__((always_inline)) {
-      constexpr bool WHOLE = decltype(whole_t)::value != 0;
+      constexpr bool WHOLE = decltype(whole_t)::value != 0;  // of the columns
 #pragma unroll
       for (int h = 0; h < FB; ++h) {
         const int r0 = wb * (BT / 2) + 16 * h;  // the fragment's first row in the tile
+        if (r0 >= t.b_rows) continue;
         const float w = !DW && a.row_w ? scale[r0 + l16] : 1.f;
         const int r = r0 + (lane >> 2);  // the row that this lane stores
-        const bool in = WHOLE || r < t.b_rows;
         const int64_t at =
             ((DW ? static_cast<int64_t>(t.e) * a.nb : static_cast<int64_t>(t.r0)) + t.bt * BT + r) * a.out_ld;
 #pragma unroll
@@ -603,14 +628,16 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
           o.set(v);
           o.by_row();
           const int col = t.ct * kCols + (SWIGLU ? 32 : 64) * wa + Out::kCols * (4 * c + (lane & 3));
-          if (WHOLE || (in && col < a.na)) o.template store<WHOLE>(a, at, col);
+          if (r < t.b_rows && (WHOLE || col < a.na)) o.template store<WHOLE>(a, at, col);
         }
       }
     };
-    if (a.out_vec && t.b_rows >= BT && (t.ct + 1) * kCols <= a.na) {
+    if (a.out_vec && (t.ct + 1) * kCols <= a.na) {
       store_tile(IntC<1>{});
+      if (t.b_rows >= BT) {  // none of the stores was skipped
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) after[k] += kStores;
+        for (int k = 0; k < kAhead; ++k) after[k] += kStores;
+      }
     } else {
       store_tile(IntC<0>{});
     }
