@@ -48,6 +48,7 @@ MOE_DEV f32x4_t mfma_mx(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c, ui
 // the last place of fp32, 6 instructions for 29 of expf and a division (a
 // tile's epilogue 6500 -> 2600 cycles).  exp(-g) overflows to infinity and
 // the reciprocal to 0 as in the exact form; -inf gives NaN as 0 * inf does.
+// Below g = -87 the result, under 2^-118 |u|, may become 0.
 MOE_DEV float swiglu(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
 // Results on their way to memory: W words of one output row's neighbouring

@@ -104,6 +104,19 @@ def test_mx_quantize_non_finite_denormal_and_zero_blocks(mb):
     assert torch.equal(out.cpu().isnan(), gu.mx_decode(*gu.mx_encode(x), 160).isnan())
 
 
+def test_mx_dequantize_every_code_and_scale(mb):
+    """All 16 codes under all 256 scales, in the three types: exact but for the type's own rounding."""
+    say("dequantise: every code and scale")
+    q = torch.zeros(256, 64, dtype=torch.uint8)
+    q[:, :8] = torch.arange(8, dtype=torch.uint8) * 2 + (torch.arange(8, dtype=torch.uint8) * 2 + 1) * 16
+    s = torch.arange(256, dtype=torch.uint8)[:, None].expand(256, 4).contiguous()
+    want = gu.mx_decode(q, s, 16)
+    for dtype in (F32, BF, HF):
+        out = torch.empty(256, 16, dtype=dtype, device="cuda")
+        mb.mx_dequantize(q.cuda(), s.cuda(), out)
+        assert torch.equal(torch.nan_to_num(out.cpu(), nan=77.0), torch.nan_to_num(want.to(dtype), nan=77.0))
+
+
 # ---- grouped products -----------------------------------------------------------
 
 def cases():
@@ -260,6 +273,122 @@ def test_mx_grouped_gemm(mb, label, N, K, swiglu, out_dtype):
         assert bool(((got - y).abs()[used] <= limit[used]).all())
         pad = out.as_strided((n_rows, 5 if N % 2 else 8), (out.stride(0), 1), N)
         assert bool((pad == 7.0).all())
+
+
+@pytest.mark.parametrize("op", ["gemm", "gemm_dx", "gemm_dw"])
+@pytest.mark.parametrize("dtype,out_dtype", [(BF, F32), (HF, HF)])
+def test_many_tiles(mb, op, dtype, out_dtype):
+    """Calls of more than four wide tiles a compute unit, and of more than 32 for a block; widths that end inside one."""
+    say(f"many tiles {op} {dtype}")
+    g = torch.Generator().manual_seed(31)
+    for E, wide, other, rows in ((1024, 2312, 16, 1060), (40, 7048, 72, 900)):
+        counts = torch.bincount(torch.randint(0, E, (rows,), generator=g), minlength=E)
+        off = torch.cat([torch.zeros(1), counts.cumsum(0)]).to(torch.int32)
+        N, K = (other, wide) if op == "gemm_dx" else (wide, other)
+        x = torch.randn(rows, K, generator=g).to(dtype)
+        dy = torch.randn(rows, N, generator=g).to(dtype)
+        w = torch.randn(E, N, K, generator=g).to(dtype)
+        if op == "gemm_dw":
+            out = torch.full((E, N, K), 7.0, dtype=out_dtype, device="cuda")
+            mb.grouped_gemm_dw(dev(dy), dev(x), dev(off), out)
+            for e, a, b in gu.groups(off, rows, E):
+                ref = dy[a:b].double().T @ x[a:b].double()
+                mag = dy[a:b].double().abs().T @ x[a:b].double().abs()
+                limit = gu.rounded(ref, gu.sum_bound(mag, max(1, b - a), 32), out_dtype)
+                assert bool(((out[e].cpu().double() - ref).abs() <= limit).all())
+            continue
+        out = torch.full((rows, wide), 7.0, dtype=out_dtype, device="cuda")
+        if op == "gemm":
+            mb.grouped_gemm(dev(x), dev(w), dev(off), out)
+            y, m = gu.product(x.double(), w.double(), off, rows)
+        else:
+            mb.grouped_gemm_dx(dev(dy), dev(w), dev(off), out)
+            y, m = gu.product(dy.double(), w.double().transpose(1, 2), off, rows)
+        check(out, y, m, gu.in_groups(off, rows), out_dtype, other, 32, f"E={E}")
+
+
+def test_mx_many_tiles(mb):
+    """More than 32 tiles a block; codes and scales drawn as bytes."""
+    say("MXFP4, many tiles")
+    g = torch.Generator().manual_seed(33)
+    E, N, K, rows = 1024, 1092, 40, 1100
+    off = torch.cat([torch.zeros(1), torch.bincount(torch.randint(0, E, (rows,), generator=g), minlength=E).cumsum(0)]).to(torch.int32)
+
+    def draw(n):
+        q = torch.randint(0, 256, (n, 64), generator=g, dtype=torch.uint8)
+        q[:, K // 2:] = 0
+        return q, torch.randint(120, 130, (n, 4), generator=g, dtype=torch.uint8)
+
+    x, w, up = draw(rows), draw(E * N), draw(E * N)
+    out = torch.full((rows, N), 7.0, device="cuda")
+    mb.mx_grouped_gemm(tuple(map(dev, x)), tuple(map(dev, w)), E, K, dev(off), out, up=tuple(map(dev, up)))
+    xr = gu.mx_decode(*x, K)
+    y, m = gu.product(xr, gu.mx_decode(*w, K).reshape(E, N, K), off, rows)
+    u, mu = gu.product(xr, gu.mx_decode(*up, K).reshape(E, N, K), off, rows)
+    m, mu, a = gu.sum_bound(m, K, 128), gu.sum_bound(mu, K, 128), gu.silu(y)
+    m = 1.1 * m * (u.abs() + mu) + (a.abs() + 1.1 * m) * mu + 2.0 ** -20 * (a * u).abs()
+    # below -87 the exponential leaves fp32 and the result, at most 2^-118 of u, may become zero
+    m = m + torch.where(y < -80, 2.0 ** -100 * u.abs(), 0.0)
+    assert bool(((out.cpu().double() - a * u).abs() <= gu.rounded(a * u, m, F32)).all())
+
+
+def test_places_past_32_bits(mb):
+    """Rows and matrices that lie more than 2^32 bytes into their arrays."""
+    say("places past 32 bits")
+    g = torch.Generator().manual_seed(35)
+    K, T = 2048, (1 << 20) + 64  # 4.3 GB of rows
+    x = torch.empty(T, K, dtype=BF, device="cuda")
+    at = torch.tensor([T - 1, 5, T - 64, 1 << 19], dtype=torch.int32)
+    rows = torch.randn(4, K, generator=g).to(BF)
+    x[at.long().cuda()] = dev(rows)
+    E, N = 600, 2048  # 5 GB of matrices
+    w = torch.empty(E, N, K, dtype=BF, device="cuda")
+    used = torch.randn(2, N, K, generator=g).to(BF)
+    w[3], w[E - 1] = dev(used[0]), dev(used[1])
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts[3], counts[E - 1] = 1, 3
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)]).to(torch.int32)
+    ref = torch.cat([rows[:1].double() @ used[0].double().T, rows[1:].double() @ used[1].double().T])
+    mag = torch.cat([rows[:1].double().abs() @ used[0].double().abs().T, rows[1:].double().abs() @ used[1].double().abs().T])
+    limit = gu.rounded(ref, gu.sum_bound(mag, K, 32), F32)
+    for more in (0, 300):  # the few-row kernel, and the tiles (with rows of token 5 for company)
+        tok = torch.cat([torch.full((more,), 5, dtype=torch.int32), at])
+        offsets = off + more * (torch.arange(E + 1) > 0).to(torch.int32)
+        out = torch.empty(4 + more, N, device="cuda")
+        w[0] = 0
+        mb.grouped_gemm(x, w, dev(offsets.to(torch.int32)), out, row_tok=dev(tok))
+        assert bool(((out[more:].cpu().double() - ref).abs() <= limit).all())
+    dy = torch.randn(4, N, generator=g).to(BF)
+    dx = torch.empty(4, K, device="cuda")
+    mb.grouped_gemm_dx(dev(dy), w, dev(off), dx)
+    ref = torch.cat([dy[:1].double() @ used[0].double(), dy[1:].double() @ used[1].double()])
+    mag = torch.cat([dy[:1].double().abs() @ used[0].double().abs(), dy[1:].double().abs() @ used[1].double().abs()])
+    assert bool(((dx.cpu().double() - ref).abs() <= gu.rounded(ref, gu.sum_bound(mag, N, 32), F32)).all())
+    del w
+    dw = torch.full((E, N, K), 7.0, dtype=BF, device="cuda")
+    mb.grouped_gemm_dw(dev(dy), x, dev(off), dw, row_tok=dev(at))
+    ref = dy[1:].double().T @ rows[1:].double()
+    mag = dy[1:].double().abs().T @ rows[1:].double().abs()
+    assert bool(((dw[E - 1].cpu().double() - ref).abs() <= gu.rounded(ref, gu.sum_bound(mag, 3, 32), BF)).all())
+    assert not bool(dw[E - 2].any())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_small_and_large_values(mb, dtype):
+    """Denormal 16-bit values count, infinities and NaN spread as the sums do."""
+    say(f"denormals, infinities {dtype}")
+    for rows in (4, 300):
+        tiny = torch.finfo(dtype).smallest_normal / 4
+        x = torch.full((rows, 64), tiny, dtype=dtype)
+        w = torch.full((1, 16, 64), 1.0 if dtype == HF else 2.0 ** 20, dtype=dtype)
+        out = torch.empty(rows, 16, device="cuda")
+        mb.grouped_gemm(dev(x), dev(w), None, out)
+        assert torch.equal(out.cpu().double(), x.double() @ w[0].double().T)
+        x = torch.ones(rows, 64, dtype=dtype)
+        x[1, 3], x[2, 5], x[3, 7], x[3, 8] = float("inf"), float("nan"), float("inf"), float("-inf")
+        mb.grouped_gemm(dev(x), dev(w), None, out)
+        got = out.cpu()
+        assert bool((got[1] == float("inf")).all()) and bool(got[2:4].isnan().all()) and bool(got[0].isfinite().all())
 
 
 def test_mx_nan_blocks_reach_only_their_sums(mb):
