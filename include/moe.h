@@ -401,14 +401,21 @@ int moe_grouped_gemm_dx(const void *dy, int64_t dy_ld, int32_t n_rows, const voi
                         int32_t N, int32_t K, const int32_t *offsets, void *dx, int32_t out_type, int64_t dx_ld,
                         void *stream);
 
+/* Bytes of workspace moe_grouped_gemm_dw needs (host, pure): 0 unless few
+ * and small matrices get many rows (a shared expert's, say), whose rows are
+ * then summed in parts. */
+size_t moe_grouped_gemm_dw_workspace_bytes(int32_t n_rows, int32_t E, int32_t N, int32_t K);
+
 /* Its gradient by the matrices: dw[e][n][k] = sum over the rows r of expert
  * e of dy[r][n] x[r][k] (dense [E][N][K]); an expert without rows gets
  * zeros, also when n_rows = 0 (dy, x and row_tok may then be NULL).  The
- * sums run over r in order of the matrix cores' blocks, the same for
- * identical inputs. */
+ * sums are made in the same order for identical inputs.  ws: 256-byte
+ * aligned, moe_grouped_gemm_dw_workspace_bytes(n_rows, E, N, K) bytes, or
+ * NULL where that is 0; MOE_ERR_WORKSPACE if it is needed and missing,
+ * misaligned or too small. */
 int moe_grouped_gemm_dw(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, int32_t T, int32_t n_rows,
                         int32_t type, int32_t E, int32_t N, int32_t K, const int32_t *offsets,
-                        const int32_t *row_tok, void *dw, int32_t out_type, void *stream);
+                        const int32_t *row_tok, void *dw, int32_t out_type, void *ws, size_t ws_bytes, void *stream);
 
 /* ---- Measurement helpers (not on the layer path) ----
  *

@@ -96,8 +96,9 @@ _SIGS = {
     "moe_grouped_gemm": ([_vp, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _vp],
                          ctypes.c_int),
     "moe_grouped_gemm_dx": ([_vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i64, _vp], ctypes.c_int),
-    "moe_grouped_gemm_dw": ([_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp],
-                            ctypes.c_int),
+    "moe_grouped_gemm_dw_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "moe_grouped_gemm_dw": ([_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _sz,
+                             _vp], ctypes.c_int),
     "moe_calib_read": ([_vp, _sz, ctypes.POINTER(ctypes.c_float), _vp], ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
@@ -455,16 +456,27 @@ def grouped_gemm_dx(dy: torch.Tensor, w: torch.Tensor, offsets, dx: torch.Tensor
           _dense(offsets, "offsets", torch.int32, E + 1, dev), op, okind, out_ld)
 
 
-def grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, offsets, dw: torch.Tensor, row_tok=None, stream=None):
-    """moe_grouped_gemm_dw: dw [E][N][K] from dy [n_rows][N] and rows x [T][K]."""
+def grouped_gemm_dw_workspace_bytes(n_rows: int, E: int, N: int, K: int) -> int:
+    return int(_lib.moe_grouped_gemm_dw_workspace_bytes(n_rows, E, N, K))
+
+
+def grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, offsets, dw: torch.Tensor, row_tok=None, stream=None, ws=None):
+    """moe_grouped_gemm_dw: dw [E][N][K] from dy [n_rows][N] and rows x [T][K].  ws None: a workspace of
+    grouped_gemm_dw_workspace_bytes is allocated here when the call needs one."""
     yp, y_ld, n_rows, N, kind, dev = _rows(dy, "dy")
     xp, x_ld, T, K, xkind, xdev = _rows(x, "x")
     op, E, on, ok, okind = _weights(dw, "dw", dev)
     if xkind != kind or on != N or ok != K or xdev != dev:
         raise ValueError("dy [n_rows][N], x [T][K] (of one type) and dw [E][N][K] do not fit")
+    need = _lib.moe_grouped_gemm_dw_workspace_bytes(n_rows, E, N, K)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        if stream is not None:
+            ws.record_stream(stream)
+    wp = _dense(ws, "ws", torch.uint8, need, dev)
     _call("moe_grouped_gemm_dw", dev, stream, yp, y_ld, xp, x_ld, T, n_rows, kind, E, N, K,
           _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),
-          op, okind)
+          op, okind, wp, 0 if ws is None else ws.numel())
 
 
 def calib_mfma(kind: int, iters: int, stream=None):

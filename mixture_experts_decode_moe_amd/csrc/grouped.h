@@ -47,8 +47,11 @@ struct GroupedArgs {
   char *out;
   int64_t out_ld;        // elements
   int32_t out_vec;       // out rows are 16-byte aligned
+  int32_t splits;        // dw: parts of a group's rows (1: none)
+  char *parts;           // dw with parts: float [splits][E][nb][na]
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s);
+int32_t grouped_dw_splits(int32_t n_rows, int32_t E, int32_t N, int32_t K);
 // fwd and mx with few rows an expert
 hipError_t launch_grouped_few(const GroupedArgs &a, hipStream_t s);
 

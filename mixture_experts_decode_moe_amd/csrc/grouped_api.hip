@@ -1,6 +1,6 @@
 // Host side of the grouped products and the MXFP4 conversions: argument
-// checks, then one launch.  Nothing here or in their kernels needs a
-// workspace, keeps state or allocates.
+// checks, then one launch (two for a split dw, whose parts take the only
+// workspace here).  Nothing keeps state or allocates.
 #include <stdint.h>
 
 #include "grouped.h"
@@ -70,6 +70,7 @@ GroupedArgs grouped_args(int32_t kind, int32_t type, int32_t out_type, int32_t T
   a.row_w = row_w;
   a.out = static_cast<char *>(out);
   a.out_ld = out_ld;
+  a.splits = 1;
   a.out_vec = aligned(out, 16) && (out_ld * type_size(out_type)) % 16 == 0;
   return a;
 }
@@ -169,9 +170,15 @@ int moe_grouped_gemm_dx(const void *dy, int64_t dy_ld, int32_t n_rows, const voi
   return hip_status(launch_grouped(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_grouped_gemm_dw_workspace_bytes(int32_t n_rows, int32_t E, int32_t N, int32_t K) {
+  if (n_rows < 0 || E <= 0 || N <= 0 || K <= 0 || E > 1024 || N > kMaxWidth || K > kMaxWidth) return 0;
+  const int32_t parts = grouped_dw_splits(n_rows, E, N, K);
+  return parts > 1 ? align_up(static_cast<size_t>(parts) * E * N * K * sizeof(float), 256) : 0;
+}
+
 int moe_grouped_gemm_dw(const void *dy, int64_t dy_ld, const void *x, int64_t x_ld, int32_t T, int32_t n_rows,
                         int32_t type, int32_t E, int32_t N, int32_t K, const int32_t *offsets,
-                        const int32_t *row_tok, void *dw, int32_t out_type, void *stream) {
+                        const int32_t *row_tok, void *dw, int32_t out_type, void *ws, size_t ws_bytes, void *stream) {
   int rc = check_groups(n_rows, E, N, K, offsets);
   if (rc == MOE_OK) rc = check_16bit(type, out_type, N, K);
   if (rc == MOE_OK) rc = check_rows(x, T, n_rows, row_tok, nullptr);
@@ -187,6 +194,12 @@ int moe_grouped_gemm_dw(const void *dy, int64_t dy_ld, const void *x, int64_t x_
   a.b_ld = 2 * dy_ld;
   a.na = K;
   a.nb = N;
+  const size_t need = moe_grouped_gemm_dw_workspace_bytes(n_rows, E, N, K);
+  if (need > 0) {
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    a.splits = grouped_dw_splits(n_rows, E, N, K);
+    a.parts = static_cast<char *>(ws);
+  }
   return hip_status(launch_grouped(a, static_cast<hipStream_t>(stream)));
 }
 

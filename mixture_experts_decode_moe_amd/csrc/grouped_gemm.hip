@@ -143,14 +143,16 @@ struct Tile {
   int steps;
 };
 
-template <int KIND, int TYPE, int OUT, int CT, int STAGES, bool SWIGLU>
-__global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
-  constexpr int NT = 2 * CT, NW = NT / 64;  // CT / 64 x 2 waves of 64 x 64 results
+template <int KIND, int TYPE, int OUT, int CT, int NW, int STAGES, bool SWIGLU>
+__global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
+  // dw: group e's rows in a.splits parts, part p of it the `expert` p E + e
+  constexpr int NT = 64 * NW;
+  constexpr int kWaveRows = kGrRows * CT / 64 / NW;  // results of a wave: so many rows, 64 columns
   constexpr int BT = kGrRows;
   constexpr bool MX = KIND == kGroupedMx, DW = KIND == kGroupedDw;
   constexpr bool ACROSS_A = KIND == kGroupedDx || DW, ACROSS_B = DW;  // reduction across the operand's rows
   constexpr int NA = CT / 8 / NW, NB = BT / 8 / NW;                   // 1 KB requests a wave, a step
-  constexpr int FB = BT / 32;                                         // 16-row fragments of a wave along b
+  constexpr int FB = kWaveRows / 16;                                  // 16-row fragments of a wave
   constexpr int kAhead = STAGES - 1;                                  // steps requested before they are multiplied
   constexpr int kCols = SWIGLU ? CT / 2 : CT;
   constexpr uint32_t kDataA = CT * kGrStep, kDataB = BT * kGrStep;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
   const uint32_t scale0 = __builtin_amdgcn_readfirstlane(lds_addr(row_scale));
 
   group_table<!DW, NT>(a, lo, pre, scratch);
-  const int n_items = DW ? a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[a.E]) * col_tiles;
+  const int n_items = DW ? a.splits * a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[a.E]) * col_tiles;
   // Blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items,
   // its blocks in turn.  (Ranges of their own for 16, 8, 4 or 1 of the blocks
   // lose the sharing in the L2: dw 606 -> 796, 784, 841, 1110 us.)
@@ -214,8 +216,14 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
       const int in = item - t.e * (col_tiles * dw_tiles);
       t.bt = in / col_tiles;
       t.ct = in - t.bt * col_tiles;
-      t.r0 = __builtin_amdgcn_readfirstlane(lo[t.e]);
-      t.n = max(__builtin_amdgcn_readfirstlane(lo[t.e + 1]) - t.r0, 0);
+      const int part = t.e / a.E, e = t.e - part * a.E;
+      t.r0 = __builtin_amdgcn_readfirstlane(lo[e]);
+      t.n = max(__builtin_amdgcn_readfirstlane(lo[e + 1]) - t.r0, 0);
+      if (a.splits > 1) {
+        const int rows = ((t.n + kGrRed - 1) / kGrRed + a.splits - 1) / a.splits * kGrRed;  // of a part
+        t.r0 += min(part * rows, t.n);
+        t.n = min(rows, max(t.n - part * rows, 0));
+      }
     } else {
       const int4 v = table[i & (2 * kTableTiles - 1)];
       const int ec = __builtin_amdgcn_readfirstlane(v.x);
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
 #pragma unroll
       for (int h = 0; h < FB; ++h) acc[f][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    const int fragments = (t.b_rows - wb * (BT / 2) + 15) >> 4;  // of this wave that have rows, or more than FB
+    const int fragments = (t.b_rows - wb * kWaveRows + 15) >> 4;  // of this wave that have rows, or more than FB
     for (int s = 0; s < t.steps; ++s) {
       if (after[0] >= kRequests + kStores)
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(kRequests + kStores));
@@ -567,9 +575,9 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
           }
 #pragma unroll
           for (int h = 0; h < NF; ++h) {
-            const int R = wb * (BT / 2) + 16 * h + l16;
+            const int R = wb * kWaveRows + 16 * h + l16;
             if constexpr (ACROSS_B) {
-              B[h] = across(tb, 2 * BT, wb * (BT / 2) + 16 * h, -1);
+              B[h] = across(tb, 2 * BT, wb * kWaveRows + 16 * h, -1);
             } else {
               B[h] = along(tb, R, swz<false>(R));
               if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 16 * (CT + R) + 4 * kk) >> (8 * g);
@@ -592,10 +600,10 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
         read(1);
         multiply();
       };
-      if (fragments > 2)
-        step(IntC<4>{});
-      else if (fragments == 2)
-        step(IntC<2>{});
+      if (fragments > FB / 2)
+        step(IntC<FB>{});
+      else if (FB > 2 && fragments == 2)
+        step(IntC<(FB > 2 ? 2 : 0)>{});
       else if (fragments == 1)
         step(IntC<1>{});
       else
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
       constexpr bool WHOLE = decltype(whole_t)::value != 0;  // of the columns
 #pragma unroll
       for (int h = 0; h < FB; ++h) {
-        const int r0 = wb * (BT / 2) + 16 * h;  // the fragment's first row in the tile
+        const int r0 = wb * kWaveRows + 16 * h;  // the fragment's first row in the tile
         if (r0 >= t.b_rows) continue;
         const float w = !DW && a.row_w ? scale[r0 + l16] : 1.f;
         const int r = r0 + (lane >> 2);  // the row that this lane stores
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(2 * CT, 2) grouped_tile_kernel(GroupedArgs a, 
 struct TileCount {
   int32_t col_tiles, dw_tiles;
   int64_t tiles;
-  TileCount(const GroupedArgs &a, int32_t cols) {
+  TileCount(const GroupedArgs &a, int32_t cols) {  // dw: of one part
     col_tiles = (a.na + cols - 1) / cols;
     dw_tiles = (a.nb + kGrRows - 1) / kGrRows;
     const int64_t rows = a.kind == kGroupedDw ? static_cast<int64_t>(a.E) * dw_tiles
@@ -657,14 +665,14 @@ struct TileCount {
   }
 };
 
-template <int KIND, int TYPE, int OUT, int CT, int STAGES, bool SWIGLU>
+template <int KIND, int TYPE, int OUT, int CT, int NW, int STAGES, bool SWIGLU>
 hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
   const TileCount n(a, SWIGLU ? CT / 2 : CT);
-  constexpr int64_t kMost = CT == 128 ? 512 : 256;  // blocks that the compute units hold
-  const int64_t blocks = (n.tiles + 7) / 8 * 8;
+  constexpr int64_t kMost = NW == 4 ? 512 : 256;  // blocks that the compute units hold
+  const int64_t blocks = (n.tiles * (KIND == kGroupedDw ? a.splits : 1) + 7) / 8 * 8;
   const uint32_t lds = (a.E + 1) * sizeof(int) * (KIND == kGroupedDw ? 1 : 2);
-  grouped_tile_kernel<KIND, TYPE, OUT, CT, STAGES, SWIGLU>
-      <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), 2 * CT, lds, s>>>(a, n.col_tiles, n.dw_tiles);
+  grouped_tile_kernel<KIND, TYPE, OUT, CT, NW, STAGES, SWIGLU>
+      <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), 64 * NW, lds, s>>>(a, n.col_tiles, n.dw_tiles);
   return hipGetLastError();
 }
 
@@ -677,10 +685,21 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
 // 512 rows over eight experts of 2048 x 2048 fwd 29.0 against 34.7, dw of one
 // expert 106 against 139.  MXFP4's scales leave the wide tile no third buffer,
 // and with two it loses (gate/up of 16384 rows 91 against 80 us).
+//
+// With at most one tile a compute unit the narrow tile gets a block of eight
+// waves of 64 x 32 results and three buffers: half the requests and products
+// a wave in each step (fwd of 300 rows over eight experts of 1024 x 1024 15.7
+// -> 12.7 us, MXFP4 8.0 -> 7.2, dw of 16384 rows and one 2048 x 2048 matrix 257
+// -> 188); with more tiles two blocks of four waves are better (4096 rows over
+// eight experts 20.7 against 27.4).
+constexpr int64_t kWideTiles = 1024, kLoneTiles = 256;
+
 template <int KIND, int TYPE, int OUT>
 hipError_t launch_width(const GroupedArgs &a, hipStream_t s) {
-  return TileCount(a, 256).tiles >= 1024 ? launch_tile<KIND, TYPE, OUT, 256, 3, false>(a, s)
-                                         : launch_tile<KIND, TYPE, OUT, 128, 2, false>(a, s);
+  const int64_t parts = KIND == kGroupedDw ? a.splits : 1;
+  if (TileCount(a, 256).tiles * parts >= kWideTiles) return launch_tile<KIND, TYPE, OUT, 256, 8, 3, false>(a, s);
+  return TileCount(a, 128).tiles * parts <= kLoneTiles ? launch_tile<KIND, TYPE, OUT, 128, 8, 3, false>(a, s)
+                                                       : launch_tile<KIND, TYPE, OUT, 128, 4, 2, false>(a, s);
 }
 
 template <int KIND>
@@ -692,16 +711,15 @@ hipError_t launch_16bit(const GroupedArgs &a, hipStream_t s) {
                                  : launch_width<KIND, MOE_T_F16, MOE_T_F16>(a, s);
 }
 
-template <bool SWIGLU>
+template <int OUT, bool SWIGLU>
 hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
-  switch (a.out_type) {
-    case MOE_T_BF16:
-      return launch_tile<kGroupedMx, 0, MOE_T_BF16, 128, 2, SWIGLU>(a, s);
-    case MOE_T_F16:
-      return launch_tile<kGroupedMx, 0, MOE_T_F16, 128, 2, SWIGLU>(a, s);
-    default:
-      return launch_tile<kGroupedMx, 0, MOE_T_F32, 128, 2, SWIGLU>(a, s);
-  }
+  return TileCount(a, SWIGLU ? 64 : 128).tiles <= kLoneTiles ? launch_tile<kGroupedMx, 0, OUT, 128, 8, 3, SWIGLU>(a, s)
+                                                             : launch_tile<kGroupedMx, 0, OUT, 128, 4, 2, SWIGLU>(a, s);
+}
+
+template <int OUT>
+hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
+  return a.a2 ? launch_mx<OUT, true>(a, s) : launch_mx<OUT, false>(a, s);
 }
 
 // Whether the few-row kernel takes the call: up to 256 rows, and tiles for
@@ -716,17 +734,74 @@ bool few_rows(const GroupedArgs &a) {
   return (a.kind == kGroupedFwd || a.kind == kGroupedMx) && a.n_rows <= 256 && TileCount(a, a.a2 ? 64 : 128).tiles <= 256;
 }
 
+// dw[i] = the sum of its parts, in order
+template <int OUT>
+__global__ void __launch_bounds__(256) grouped_join_kernel(const float4 *__restrict__ part, int32_t splits, int64_t n4,
+                                                           char *__restrict__ out) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4; i += static_cast<int64_t>(gridDim.x) * 256) {
+    float4 v = part[i];
+    for (int p = 1; p < splits; ++p) {
+      const float4 w = part[p * n4 + i];
+      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+    Packed<OUT, OUT == MOE_T_F32 ? 4 : 2> o;
+    const float u[4] = {v.x, v.y, v.z, v.w};
+    o.set(u);
+    if constexpr (OUT == MOE_T_F32)
+      reinterpret_cast<uint4 *>(out)[i] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+    else
+      reinterpret_cast<uint2 *>(out)[i] = make_uint2(o.w[0], o.w[1]);
+  }
+}
+
+hipError_t launch_dw_split(const GroupedArgs &a, hipStream_t s) {
+  GroupedArgs p = a;
+  p.out = a.parts;
+  p.out_type = MOE_T_F32;
+  p.out_vec = 1;
+  hipError_t e = launch_16bit<kGroupedDw>(p, s);
+  if (e != hipSuccess) return e;
+  const int64_t n4 = static_cast<int64_t>(a.E) * a.nb * a.na / 4;
+  const int64_t blocks = (n4 + 255) / 256;
+  const dim3 grid(static_cast<uint32_t>(blocks < 2048 ? blocks : 2048));
+  const float4 *part = reinterpret_cast<const float4 *>(a.parts);
+  switch (a.out_type) {
+    case MOE_T_BF16:
+      grouped_join_kernel<MOE_T_BF16><<<grid, 256, 0, s>>>(part, a.splits, n4, a.out);
+      break;
+    case MOE_T_F16:
+      grouped_join_kernel<MOE_T_F16><<<grid, 256, 0, s>>>(part, a.splits, n4, a.out);
+      break;
+    default:
+      grouped_join_kernel<MOE_T_F32><<<grid, 256, 0, s>>>(part, a.splits, n4, a.out);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
+
+// Parts for dw: where its tiles leave half of the compute units or more
+// without one, as many as fill them, of 256 rows or more on average (a shared
+// expert's gradient: one 512 x 512 matrix with 16384 rows is 16 tiles of 256
+// steps: 188 us whole, 26 in 16 parts with their sum).
+int32_t grouped_dw_splits(int32_t n_rows, int32_t E, int32_t N, int32_t K) {
+  const int64_t tiles = static_cast<int64_t>(E) * ((N + kGrRows - 1) / kGrRows) * ((K + 127) / 128);
+  const int64_t by_tiles = kLoneTiles / tiles, by_rows = n_rows / E / 256;
+  const int64_t n = by_tiles < by_rows ? by_tiles : by_rows;
+  return static_cast<int32_t>(n < 1 ? 1 : n > 16 ? 16 : n);
+}
 
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s) {
   if (few_rows(a)) return launch_grouped_few(a, s);
   switch (a.kind) {
     case kGroupedMx:
-      return a.a2 ? launch_mx<true>(a, s) : launch_mx<false>(a, s);
+      return a.out_type == MOE_T_BF16  ? launch_mx<MOE_T_BF16>(a, s)
+             : a.out_type == MOE_T_F16 ? launch_mx<MOE_T_F16>(a, s)
+                                       : launch_mx<MOE_T_F32>(a, s);
     case kGroupedDx:
       return launch_16bit<kGroupedDx>(a, s);
     case kGroupedDw:
-      return launch_16bit<kGroupedDw>(a, s);
+      return a.splits > 1 ? launch_dw_split(a, s) : launch_16bit<kGroupedDw>(a, s);
     default:
       return launch_16bit<kGroupedFwd>(a, s);
   }

@@ -225,6 +225,41 @@ def test_grouped_gemm_dw(mb, label, N, K, dtype, out_dtype):
         assert bool((diff <= limit).all())
 
 
+@pytest.mark.parametrize("counts,N,K,dtype,out_dtype", [([5000], 136, 264, BF, BF), ([3001], 8, 8, HF, F32),
+                                                        ([4000, 0, 17, 2300], 128, 200, HF, HF)])
+def test_grouped_gemm_dw_in_parts(mb, counts, N, K, dtype, out_dtype):
+    """Few small matrices with many rows: the rows are summed in parts; ragged, empty and short groups; a workspace of the
+    caller's, and a graph."""
+    rows, E = sum(counts), len(counts)
+    say(f"dw in parts {counts} N={N} K={K}")
+    need = mb.grouped_gemm_dw_workspace_bytes(rows, E, N, K)
+    assert need > 0
+    g = torch.Generator().manual_seed(rows)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    tok = tokens(rows, 700, 6)
+    x, dy = torch.randn(700, K, generator=g).to(dtype), torch.randn(rows, N, generator=g).to(dtype)
+    xr = gu.gathered(x, tok, rows)
+    ref = torch.stack([dy[a:b].double().T @ xr[a:b] for _, a, b in gu.groups(off, rows, E)])
+    mag = torch.stack([dy[a:b].double().abs().T @ xr[a:b].abs() for _, a, b in gu.groups(off, rows, E)])
+    args = dev(dy), dev(x), dev(off)
+    out = torch.full((E, N, K), 7.0, dtype=out_dtype, device="cuda")
+    mb.grouped_gemm_dw(*args, out, row_tok=dev(tok))
+    # a part is a shorter sum; the parts are at most 16 more additions
+    limit = gu.rounded(ref, gu.sum_bound(mag, rows, 32) + 16 * 2.0 ** -24 * mag, out_dtype)
+    assert bool(((out.cpu().double() - ref).abs() <= limit).all())
+    first = out.clone()
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    t = dev(tok)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mb.grouped_gemm_dw(*args, out, row_tok=t, ws=ws)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first) and bool((ws[need:] == 0xFF).all())
+
+
 def test_grouped_gemm_dw_without_rows_is_zero(mb):
     say("dw, n_rows = 0")
     out = torch.full((3, 16, 24), 7.0, device="cuda")

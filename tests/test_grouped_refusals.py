@@ -73,7 +73,8 @@ def test_mx_grouped_gemm_refusals(mb, lib):
 F = dict(x=P, x_ld=64, T=4, n_rows=4, w=P, type=1, E=2, N=40, K=64, offsets=P, row_tok=None, row_w=None, out=P, out_type=3,
          out_ld=40)
 X = dict(dy=P, dy_ld=40, n_rows=4, w=P, type=2, E=2, N=40, K=64, offsets=P, dx=P, out_type=2, dx_ld=64)
-W = dict(dy=P, dy_ld=40, x=P, x_ld=64, T=4, n_rows=4, type=1, E=2, N=40, K=64, offsets=P, row_tok=None, dw=P, out_type=1)
+W = dict(dy=P, dy_ld=40, x=P, x_ld=64, T=4, n_rows=4, type=1, E=2, N=40, K=64, offsets=P, row_tok=None, dw=P, out_type=1, ws=None,
+         ws_bytes=0)
 
 
 @pytest.mark.parametrize("name,base", [("moe_grouped_gemm", F), ("moe_grouped_gemm_dx", X), ("moe_grouped_gemm_dw", W)])
@@ -115,6 +116,18 @@ def test_grouped_gemm_common_refusals(lib, name, base, kw, rc):
 ])
 def test_grouped_gemm_refusals(lib, name, base, kw, rc):
     assert call(lib, name, base, base, **kw) == rc
+
+
+def test_dw_workspace(lib):
+    """A few matrices with many rows are summed in parts: the call wants room for them, others want none."""
+    size = lib.moe_grouped_gemm_dw_workspace_bytes
+    assert size(4096, 64, 512, 1024) == 0 and size(100, 1, 64, 64) == 0 and size(0, 1, 64, 64) == 0
+    assert size(-1, 1, 64, 64) == 0 and size(4096, 0, 64, 64) == 0 and size(4096, 1, 65537, 64) == 0
+    need = size(16384, 1, 512, 520)
+    assert need >= 2 * 512 * 520 * 4
+    big = dict(T=16384, n_rows=16384, E=1, N=512, K=520, x_ld=520, dy_ld=512)
+    for kw in (dict(), dict(ws=P), dict(ws=P, ws_bytes=need - 1), dict(ws=P + 64, ws_bytes=need)):
+        assert call(lib, "moe_grouped_gemm_dw", W, W, **big, **kw) == -3
 
 
 def test_binding_refuses_host_tensors_and_wrong_kinds(mb):
