@@ -52,7 +52,9 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped(const GroupedArgs &a, hipStream_t s);
 int32_t grouped_dw_splits(int32_t n_rows, int32_t E, int32_t N, int32_t K);
-// fwd and mx with few rows an expert
+// fwd and mx with few rows an expert: the blocks such a launch has, and the
+// launch, which wants fewer than 2^31
+int64_t grouped_few_blocks(const GroupedArgs &a);
 hipError_t launch_grouped_few(const GroupedArgs &a, hipStream_t s);
 
 }  // namespace moe

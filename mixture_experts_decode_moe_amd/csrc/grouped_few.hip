@@ -3,7 +3,8 @@
 // rows, so the kernel is a stream of the weights; what counts is how soon
 // enough requests are on their way.
 //
-// An item is 16 rows of one expert by 16 columns.  A wave takes both operands
+// An item is 16 rows of one expert by 16 columns; the grid has a block for each
+// that there may be, and one without rows ends at once.  A wave takes both operands
 // straight from memory into registers: lane (l16, g) reads 16 bytes of weight
 // row l16 and of x row l16 at 64 s + 16 g, which is its operand of step s (one
 // matrix instruction: 32 16-bit elements or 128 MXFP4 elements), kUnroll
@@ -25,7 +26,15 @@ constexpr int kFewWaves = kFewThreads / 64;
 // (16-bit down of one token, eight experts of 2048 x 512)
 constexpr int kUnroll = 4;
 constexpr int kStepBytes = 64;  // of a row
-constexpr int kMaxBlocks = 256 * 8;
+
+// Whether the four waves share an item: there is a step or more for each.
+bool split(const GroupedArgs &a) { return a.red > kStepBytes * kFewWaves; }
+
+// columns' part of the grid
+int32_t col_blocks(const GroupedArgs &a) {
+  const int32_t cols = split(a) ? 16 : 16 * kFewWaves;
+  return (a.na + cols - 1) / cols;
+}
 
 // 16 rows of one expert
 struct RowTile {
@@ -80,7 +89,7 @@ MOE_DEV RowTile find_tile(const GroupedArgs &a, const Groups (&near)[kNear], int
 }
 
 template <int KIND, int TYPE, int OUT, bool SWIGLU, bool SPLIT>
-__global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a, int32_t col_blocks, int32_t max_items) {
+__global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a, int32_t col_blocks) {
   constexpr bool MX = KIND == kGroupedMx;
   constexpr int kMats = SWIGLU ? 2 : 1;
   __shared__ f32x4_t part[SPLIT ? kMats : 1][SPLIT ? kFewWaves : 1][64];
@@ -96,128 +105,118 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
   for (int i = 0; i < kNear; ++i) near[i].read(a, 64 * i);  // all on their way before any is looked at
 #pragma unroll
   for (int i = 0; i < kNear; ++i) near[i].settle(a);
-  for (int item = blockIdx.x; item < max_items; item += gridDim.x) {
-    const int j = item / col_blocks;
-    const RowTile t = find_tile(a, near, j);
-    if (t.n <= 0) break;  // the same for every wave; later items have no tile either
-    const int c0 = 16 * ((item - j * col_blocks) * (SPLIT ? 1 : kFewWaves) + (SPLIT ? 0 : wave));
-    const int col = c0 + l16;  // the weight row of this lane's operand
-    const char *pw[kMats], *ps[kMats];
+  const int item = blockIdx.x, j = item / col_blocks;
+  const RowTile t = find_tile(a, near, j);
+  if (t.n <= 0) return;  // the same for every wave
+  const int c0 = 16 * ((item - j * col_blocks) * (SPLIT ? 1 : kFewWaves) + (SPLIT ? 0 : wave));
+  const int col = c0 + l16;  // the weight row of this lane's operand
+  const char *pw[kMats], *ps[kMats];
+#pragma unroll
+  for (int m = 0; m < kMats; ++m) {
+    pw[m] = (m ? a.a2 : a.a) + static_cast<int64_t>(t.e) * a.a_expert + (col < a.na ? col : 0) * a.a_ld + 16 * g;
+    ps[m] = MX ? (m ? a.as2 : a.as) + (static_cast<int64_t>(t.e) * a.na + (col < a.na ? col : 0)) * a.s_ld + g : zero;
+  }
+  const int lim_w = col < a.na ? a.red - 16 * g : 0;
+  int src = l16 < t.n ? t.r0 + l16 : -1;
+  int tok = src;
+  if (a.row_tok && src >= 0) tok = a.row_tok[src];
+
+  // the weights of the next kUnroll steps are requested before the rows of
+  // these are needed
+  u32x4_t w[kMats][kUnroll];
+  uint32_t sw[kMats][kUnroll];
+  auto load_w = [&](int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int s = s0 + i;
+      const bool in = s < last && kStepBytes * s < lim_w;
+#pragma unroll
+      for (int m = 0; m < kMats; ++m) {
+        const uint4 v = load_stream16(reinterpret_cast<const uint4 *>(in ? pw[m] + kStepBytes * s : zero));
+        w[m][i] = u32x4_t{v.x, v.y, v.z, v.w};
+        if constexpr (MX) sw[m][i] = *reinterpret_cast<const uint8_t *>(in ? ps[m] + 4 * s : zero);
+      }
+    }
+  };
+  load_w(first);
+  if (a.row_tok) src = static_cast<uint32_t>(tok) < static_cast<uint32_t>(a.T) ? tok : -1;
+  const char *px = a.b + max(src, 0) * a.b_ld + 16 * g;
+  const char *pxs = MX ? a.bs + static_cast<int64_t>(max(src, 0)) * a.s_ld + g : zero;
+  const int lim_x = src >= 0 ? a.red - 16 * g : 0;
+
+  f32x4_t acc[kMats];
+#pragma unroll
+  for (int m = 0; m < kMats; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = first; s0 < last; s0 += kUnroll) {
+    u32x4_t x[kUnroll];
+    uint32_t sx[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int s = s0 + i;
+      const bool in = s < last && kStepBytes * s < lim_x;
+      const uint4 v = *reinterpret_cast<const uint4 *>(in ? px + kStepBytes * s : zero);
+      x[i] = u32x4_t{v.x, v.y, v.z, v.w};
+      if constexpr (MX) sx[i] = *reinterpret_cast<const uint8_t *>(in ? pxs + 4 * s : zero);
+    }
+    u32x4_t now[kMats][kUnroll];
+    uint32_t snow[kMats][kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+      for (int m = 0; m < kMats; ++m) {
+        now[m][i] = w[m][i];
+        if constexpr (MX) snow[m][i] = sw[m][i];
+      }
+    if (s0 + kUnroll < last) load_w(s0 + kUnroll);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+      for (int m = 0; m < kMats; ++m) {
+        if constexpr (MX)
+          acc[m] = mfma_mx(now[m][i], x[i], acc[m], snow[m][i], sx[i]);
+        else
+          acc[m] = mfma16<TYPE>(now[m][i], x[i], acc[m]);
+      }
+  }
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) part[m][wave][lane] = acc[m];
+    lds_barrier();
+    if (wave != 0) return;
 #pragma unroll
     for (int m = 0; m < kMats; ++m) {
-      pw[m] = (m ? a.a2 : a.a) + static_cast<int64_t>(t.e) * a.a_expert + (col < a.na ? col : 0) * a.a_ld + 16 * g;
-      ps[m] = MX ? (m ? a.as2 : a.as) + (static_cast<int64_t>(t.e) * a.na + (col < a.na ? col : 0)) * a.s_ld + g : zero;
+      acc[m] = part[m][0][lane];
+#pragma unroll
+      for (int k = 1; k < kFewWaves; ++k) acc[m] += part[m][k][lane];
     }
-    const int lim_w = col < a.na ? a.red - 16 * g : 0;
-    int src = l16 < t.n ? t.r0 + l16 : -1;
-    int tok = src;
-    if (a.row_tok && src >= 0) tok = a.row_tok[src];
-
-    // the weights of the next kUnroll steps are requested before the rows of
-    // these are needed
-    u32x4_t w[kMats][kUnroll];
-    uint32_t sw[kMats][kUnroll];
-    auto load_w = [&](int s0) __attribute__((always_inline)) {
+  }
+  // lane (l16, g): row l16, columns c0 + 4 g .. + 3
+  if (l16 < t.n && c0 + 4 * g < a.na) {
+    const int64_t row = static_cast<int64_t>(t.r0) + l16;
+    const float rw = a.row_w ? a.row_w[row] : 1.f;
+    float v[4];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int s = s0 + i;
-        const bool in = s < last && kStepBytes * s < lim_w;
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          const uint4 v = load_stream16(reinterpret_cast<const uint4 *>(in ? pw[m] + kStepBytes * s : zero));
-          w[m][i] = u32x4_t{v.x, v.y, v.z, v.w};
-          if constexpr (MX) sw[m][i] = *reinterpret_cast<const uint8_t *>(in ? ps[m] + 4 * s : zero);
-        }
-      }
-    };
-    load_w(first);
-    if (a.row_tok) src = static_cast<uint32_t>(tok) < static_cast<uint32_t>(a.T) ? tok : -1;
-    const char *px = a.b + max(src, 0) * a.b_ld + 16 * g;
-    const char *pxs = MX ? a.bs + static_cast<int64_t>(max(src, 0)) * a.s_ld + g : zero;
-    const int lim_x = src >= 0 ? a.red - 16 * g : 0;
-
-    f32x4_t acc[kMats];
-#pragma unroll
-    for (int m = 0; m < kMats; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s0 = first; s0 < last; s0 += kUnroll) {
-      u32x4_t x[kUnroll];
-      uint32_t sx[kUnroll];
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int s = s0 + i;
-        const bool in = s < last && kStepBytes * s < lim_x;
-        const uint4 v = *reinterpret_cast<const uint4 *>(in ? px + kStepBytes * s : zero);
-        x[i] = u32x4_t{v.x, v.y, v.z, v.w};
-        if constexpr (MX) sx[i] = *reinterpret_cast<const uint8_t *>(in ? pxs + 4 * s : zero);
-      }
-      u32x4_t now[kMats][kUnroll];
-      uint32_t snow[kMats][kUnroll];
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          now[m][i] = w[m][i];
-          if constexpr (MX) snow[m][i] = sw[m][i];
-        }
-      if (s0 + kUnroll < last) load_w(s0 + kUnroll);
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          if constexpr (MX)
-            acc[m] = mfma_mx(now[m][i], x[i], acc[m], snow[m][i], sx[i]);
-          else
-            acc[m] = mfma16<TYPE>(now[m][i], x[i], acc[m]);
-        }
+    for (int i = 0; i < 4; ++i) {
+      v[i] = acc[0][i];
+      if constexpr (SWIGLU) v[i] = swiglu(v[i], acc[kMats - 1][i]);
+      v[i] *= rw;
     }
-    if constexpr (SPLIT) {
-#pragma unroll
-      for (int m = 0; m < kMats; ++m) part[m][wave][lane] = acc[m];
-      lds_barrier();
-      if (wave == 0) {
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          acc[m] = part[m][0][lane];
-#pragma unroll
-          for (int k = 1; k < kFewWaves; ++k) acc[m] += part[m][k][lane];
-        }
-      }
-      lds_barrier();
-      if (wave != 0) continue;
-    }
-    // lane (l16, g): row l16, columns c0 + 4 g .. + 3
-    if (l16 < t.n && c0 + 4 * g < a.na) {
-      const int64_t row = static_cast<int64_t>(t.r0) + l16;
-      const float rw = a.row_w ? a.row_w[row] : 1.f;
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = acc[0][i];
-        if constexpr (SWIGLU) v[i] = swiglu(v[i], acc[kMats - 1][i]);
-        v[i] *= rw;
-      }
-      Packed<OUT, OUT == MOE_T_F32 ? 4 : 2> o;
-      o.set(v);
-      o.template store<false>(a, row * a.out_ld, c0 + 4 * g);
-    }
+    Packed<OUT, OUT == MOE_T_F32 ? 4 : 2> o;
+    o.set(v);
+    o.template store<false>(a, row * a.out_ld, c0 + 4 * g);
   }
 }
 
 template <int KIND, int TYPE, int OUT, bool SWIGLU, bool SPLIT>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
-  const int32_t cols = SPLIT ? 16 : 16 * kFewWaves;
-  const int32_t col_blocks = (a.na + cols - 1) / cols;
-  const int64_t items = (a.n_rows / 16 + static_cast<int64_t>(a.E < a.n_rows ? a.E : a.n_rows)) * col_blocks;
   grouped_few_kernel<KIND, TYPE, OUT, SWIGLU, SPLIT>
-      <<<dim3(static_cast<uint32_t>(items < kMaxBlocks ? items : kMaxBlocks)), kFewThreads, 0, s>>>(
-          a, col_blocks, static_cast<int32_t>(items));
+      <<<dim3(static_cast<uint32_t>(grouped_few_blocks(a))), kFewThreads, 0, s>>>(a, col_blocks(a));
   return hipGetLastError();
 }
 
 template <int KIND, int TYPE, int OUT, bool SWIGLU = false>
 hipError_t launch_by_length(const GroupedArgs &a, hipStream_t s) {
-  return a.red > kStepBytes * kFewWaves ? launch<KIND, TYPE, OUT, SWIGLU, true>(a, s)
-                                        : launch<KIND, TYPE, OUT, SWIGLU, false>(a, s);
+  return split(a) ? launch<KIND, TYPE, OUT, SWIGLU, true>(a, s) : launch<KIND, TYPE, OUT, SWIGLU, false>(a, s);
 }
 
 template <bool SWIGLU>
@@ -233,6 +232,10 @@ hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t grouped_few_blocks(const GroupedArgs &a) {
+  return (a.n_rows / 16 + static_cast<int64_t>(a.E < a.n_rows ? a.E : a.n_rows)) * col_blocks(a);
+}
 
 hipError_t launch_grouped_few(const GroupedArgs &a, hipStream_t s) {
   if (a.kind == kGroupedMx) return a.a2 ? launch_mx<true>(a, s) : launch_mx<false>(a, s);

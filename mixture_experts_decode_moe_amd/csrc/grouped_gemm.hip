@@ -722,16 +722,20 @@ hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
   return a.a2 ? launch_mx<OUT, true>(a, s) : launch_mx<OUT, false>(a, s);
 }
 
-// Whether the few-row kernel takes the call: up to 256 rows, and tiles for
-// less than one block a compute unit.  Below that the tiles leave most of the
-// chip idle and a tile's long walk is the whole time: one row each of eight
-// experts of 1024 x 2048 in 16 bits 27.9 us against 12.2, one row of a single
-// 1024 x 1024 matrix 15.7 against 4.8, 256 rows of it 15.9 against 10.3.  Above
-// it the tiles read every matrix once: 64 experts of 1024 x 1024, a row each,
-// 29.8 against 32.4 us, MXFP4 12.0 against 20.0; 1024 rows of one matrix 17.0
-// against 34.3.
+// Whether the few-row kernel takes the call: its blocks, times the matrices of
+// one, are at most five a compute unit in 16 bits, four in MXFP4.  It spreads a
+// call over the chip where tiles leave most of it idle, and its time grows with
+// its blocks; the tiles' is that of one tile's steps until they fill the chip.
+// Both grow alike with the reduction's length.  Few rows against tiles, in us:
+// 16 bits, 2048 x 2048: 64 rows (640 blocks) 11.2 / 19.7, 128 rows (1152)
+// 19.0 / 24.3, 256 rows (2176) 34.7 / 24.4; 512 x 2048: 512 rows (1056)
+// 19.1 / 24.2; sixteen of 512 x 512: 512 rows (1536) 8.5 / 8.3; eight of 256 x
+// 8192: 1024 rows (1152) 80 / 84.  MXFP4: 10.5 / 10.8, 18.0 / 10.9 and
+// 10.3 / 10.7 for 1152, 2176 and 1056; with SwiGLU 9.1 / 10.0 and 14.3 / 11.3
+// for 640 and 1152, 8.9 / 10.0 for 384 blocks of four experts.
 bool few_rows(const GroupedArgs &a) {
-  return (a.kind == kGroupedFwd || a.kind == kGroupedMx) && a.n_rows <= 256 && TileCount(a, a.a2 ? 64 : 128).tiles <= 256;
+  if (a.kind != kGroupedFwd && a.kind != kGroupedMx) return false;
+  return grouped_few_blocks(a) * (a.a2 ? 2 : 1) <= (a.kind == kGroupedMx ? 4 : 5) * 256;
 }
 
 // dw[i] = the sum of its parts, in order

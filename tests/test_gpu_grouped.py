@@ -137,6 +137,9 @@ def cases():
         ("rows outside the groups", 5, off([17, 0, 33, 2, 15], first=6), 90),
         ("decode", 64, off(torch.bincount(torch.randint(0, 64, (40,), generator=g), minlength=64).tolist()), 40),
         ("1024 experts", 1024, off(many.tolist()), int(many.sum())),
+        ("many rows", 5, off([700, 0, 1301, 1, 897], first=9), 2920),
+        ("many groups", 150, off(torch.bincount(torch.randint(0, 150, (2400,), generator=g) // 2 * 2, minlength=150)
+                                 .tolist()), 2409),
     ]
 
 
