@@ -10,29 +10,33 @@
 // matrix instruction: 32 16-bit elements or 128 MXFP4 elements), kUnroll
 // steps at once.  There is no staging to wait for and no reuse to stage for:
 // the rows are a few KB that stay in the caches.  Where the reduction is
-// long, the four waves of a block each take a quarter of one item and are
-// joined through LDS in order; where it is short, each takes an item of its
-// own.
+// long, the waves of a block each take a part of one item's and are joined
+// through LDS in order; where it is short, each takes an item of its own.
 #include "grouped_device.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kFewThreads = 256;
-constexpr int kFewWaves = kFewThreads / 64;
 // steps requested at once: 2, 4 and 8 measured 7.2, 7.0 and 7.9 us (MXFP4
 // gate/up of one token, eight experts of 512 x 2048) and 7.2, 7.3 and 11.1 us
 // (16-bit down of one token, eight experts of 2048 x 512)
 constexpr int kUnroll = 4;
 constexpr int kStepBytes = 64;  // of a row
 
-// Whether the four waves share an item: there is a step or more for each.
-bool split(const GroupedArgs &a) { return a.red > kStepBytes * kFewWaves; }
+// Waves to an item.  Up to four steps of the reduction are one round of
+// requests of one wave, and a wave with less than a round is of no use: four
+// waves from five steps on, eight from 32 (2048 bytes).  Eight against four,
+// in us: one row each of eight experts of 256 x 8192 in 16 bits 14.6 / 19.5,
+// MXFP4 7.8 / 9.1; 512 x 2048 in 16 bits 6.9 / 7.7; but MXFP4 512 x 2048 (16
+// steps) 4.8 / 4.4.  Sixteen were never ahead of eight.
+int waves(const GroupedArgs &a) {
+  return a.red >= kStepBytes * kUnroll * 8 ? 8 : a.red > kStepBytes * kUnroll ? 4 : 1;
+}
 
-// columns' part of the grid
+// Blocks to a row of the grid; without a split there are four items a block.
 int32_t col_blocks(const GroupedArgs &a) {
-  const int32_t cols = split(a) ? 16 : 16 * kFewWaves;
+  const int32_t cols = waves(a) > 1 ? 16 : 64;
   return (a.na + cols - 1) / cols;
 }
 
@@ -88,17 +92,18 @@ MOE_DEV RowTile find_tile(const GroupedArgs &a, const Groups (&near)[kNear], int
   return t;
 }
 
-template <int KIND, int TYPE, int OUT, bool SWIGLU, bool SPLIT>
-__global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a, int32_t col_blocks) {
+// SPLIT: waves to an item
+template <int KIND, int TYPE, int OUT, bool SWIGLU, int SPLIT>
+__global__ void __launch_bounds__(SPLIT > 1 ? 64 * SPLIT : 256) grouped_few_kernel(GroupedArgs a, int32_t col_blocks) {
   constexpr bool MX = KIND == kGroupedMx;
   constexpr int kMats = SWIGLU ? 2 : 1;
-  __shared__ f32x4_t part[SPLIT ? kMats : 1][SPLIT ? kFewWaves : 1][64];
+  __shared__ f32x4_t part[SPLIT > 1 ? kMats : 1][SPLIT][64];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const char *zero = reinterpret_cast<const char *>(&g_zero_page);
   const int steps = (a.red + kStepBytes - 1) / kStepBytes;
-  const int quarter = (steps + kFewWaves - 1) / kFewWaves;
-  const int first = SPLIT ? wave * quarter : 0, last = SPLIT ? min(steps, first + quarter) : steps;
+  const int share = (steps + SPLIT - 1) / SPLIT;
+  const int first = SPLIT > 1 ? wave * share : 0, last = min(steps, first + share);
 
   Groups near[kNear];
 #pragma unroll
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
   const int item = blockIdx.x, j = item / col_blocks;
   const RowTile t = find_tile(a, near, j);
   if (t.n <= 0) return;  // the same for every wave
-  const int c0 = 16 * ((item - j * col_blocks) * (SPLIT ? 1 : kFewWaves) + (SPLIT ? 0 : wave));
+  const int c0 = 16 * (SPLIT > 1 ? item - j * col_blocks : (item - j * col_blocks) * 4 + wave);
   const int col = c0 + l16;  // the weight row of this lane's operand
   const char *pw[kMats], *ps[kMats];
 #pragma unroll
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
           acc[m] = mfma16<TYPE>(now[m][i], x[i], acc[m]);
       }
   }
-  if constexpr (SPLIT) {
+  if constexpr (SPLIT > 1) {
 #pragma unroll
     for (int m = 0; m < kMats; ++m) part[m][wave][lane] = acc[m];
     lds_barrier();
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
     for (int m = 0; m < kMats; ++m) {
       acc[m] = part[m][0][lane];
 #pragma unroll
-      for (int k = 1; k < kFewWaves; ++k) acc[m] += part[m][k][lane];
+      for (int k = 1; k < SPLIT; ++k) acc[m] += part[m][k][lane];
     }
   }
   // lane (l16, g): row l16, columns c0 + 4 g .. + 3
@@ -207,16 +212,23 @@ __global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(GroupedArgs a,
   }
 }
 
-template <int KIND, int TYPE, int OUT, bool SWIGLU, bool SPLIT>
+template <int KIND, int TYPE, int OUT, bool SWIGLU, int SPLIT>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   grouped_few_kernel<KIND, TYPE, OUT, SWIGLU, SPLIT>
-      <<<dim3(static_cast<uint32_t>(grouped_few_blocks(a))), kFewThreads, 0, s>>>(a, col_blocks(a));
+      <<<dim3(static_cast<uint32_t>(grouped_few_blocks(a))), SPLIT > 1 ? 64 * SPLIT : 256, 0, s>>>(a, col_blocks(a));
   return hipGetLastError();
 }
 
 template <int KIND, int TYPE, int OUT, bool SWIGLU = false>
 hipError_t launch_by_length(const GroupedArgs &a, hipStream_t s) {
-  return split(a) ? launch<KIND, TYPE, OUT, SWIGLU, true>(a, s) : launch<KIND, TYPE, OUT, SWIGLU, false>(a, s);
+  switch (waves(a)) {
+    case 8:
+      return launch<KIND, TYPE, OUT, SWIGLU, 8>(a, s);
+    case 4:
+      return launch<KIND, TYPE, OUT, SWIGLU, 4>(a, s);
+    default:
+      return launch<KIND, TYPE, OUT, SWIGLU, 1>(a, s);
+  }
 }
 
 template <bool SWIGLU>

@@ -313,6 +313,26 @@ def test_mx_grouped_gemm(mb, label, N, K, swiglu, out_dtype):
         assert bool((pad == 7.0).all())
 
 
+@pytest.mark.parametrize("K", [1016, 1024, 1032, 4096, 5000])
+def test_long_reductions_of_few_rows(mb, K):
+    """Reductions that several waves share, the last of them with a part, a whole share or none."""
+    off = torch.tensor([0, 17, 17, 18, 40], dtype=torch.int32)
+    g = torch.Generator().manual_seed(K)
+    for dtype in (BF, HF):
+        say(f"long reductions K={K} {dtype}")
+        x, w = torch.randn(41, K, generator=g).to(dtype), (torch.randn(4, 40, K, generator=g) / K ** 0.5).to(dtype)
+        out = torch.full((41, 40), 7.0, device="cuda")
+        mb.grouped_gemm(strided(x, 8, float("nan")), dev(w), dev(off), out)
+        y, m = gu.product(x.double(), w.double(), off, 41)
+        check(out, y, m, gu.in_groups(off, 41), F32, K, 32, f"K={K}")
+    for k in (4 * K, 4 * K + 33):  # as many bytes a row, and an odd end
+        x, w = gu.mx_encode(torch.randn(41, k, generator=g)), gu.mx_encode(torch.randn(4 * 40, k, generator=g))
+        out = torch.full((41, 40), 7.0, device="cuda")
+        mb.mx_grouped_gemm((dev(x[0]), dev(x[1])), (dev(w[0]), dev(w[1])), 4, k, dev(off), out)
+        y, m = gu.product(gu.mx_decode(*x, k), gu.mx_decode(*w, k).reshape(4, 40, k), off, 41)
+        check(out, y, m, gu.in_groups(off, 41), F32, k, 128, f"MXFP4 K={k}")
+
+
 @pytest.mark.parametrize("op", ["gemm", "gemm_dx", "gemm_dw"])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF, F32), (HF, HF)])
 def test_many_tiles(mb, op, dtype, out_dtype):
