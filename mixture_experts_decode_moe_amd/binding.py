@@ -374,11 +374,15 @@ def _dense(t, name, dtype, n, dev):
     return t.data_ptr()
 
 
-def _mx(m, name, rows, cols, dev):
-    """The C struct of MXFP4 rows (q, s)."""
-    p = mx_cols(cols)
+def _mx(m, name, rows, padded, dev):
+    """The C struct of MXFP4 rows (q, s), `padded` elements each (_dense of both, in one expression)."""
     q, s = m
-    return MoeMxRows(_dense(q, name, torch.uint8, rows * (p // 2), dev), _dense(s, name, torch.uint8, rows * (p // 32), dev))
+    if (q.dtype is not torch.uint8 or s.dtype is not torch.uint8 or q.get_device() != dev or s.get_device() != dev
+            or q.numel() < rows * (padded >> 1) or s.numel() < rows * (padded >> 5)
+            or not q.is_contiguous() or not s.is_contiguous()):
+        raise ValueError(f"{name}: expected contiguous uint8 codes ({rows * (padded >> 1)}) and scales "
+                         f"({rows * (padded >> 5)}) on the other operands' device")
+    return MoeMxRows(q.data_ptr(), s.data_ptr())
 
 
 def _weights(w, name, dev):
@@ -423,9 +427,10 @@ def mx_grouped_gemm(x, w, n_experts: int, K: int, offsets, out: torch.Tensor, up
     """moe_mx_grouped_gemm: out [n_rows][N] from MXFP4 pairs (codes, scales): x (T rows), w and up (n_experts * N
     rows) of K columns each.  offsets int32 [n_experts + 1] or None (one expert)."""
     op, ld, n_rows, N, kind, dev = _rows(out, "out")
-    T = x[0].numel() // max(1, mx_cols(K) // 2)
-    xm, wm = _mx(x, "x", T, K, dev), _mx(w, "w", n_experts * N, K, dev)
-    um = None if up is None else ctypes.byref(_mx(up, "up", n_experts * N, K, dev))
+    padded = mx_cols(K)
+    T = x[0].numel() // max(1, padded >> 1)
+    xm, wm = _mx(x, "x", T, padded, dev), _mx(w, "w", n_experts * N, padded, dev)
+    um = None if up is None else ctypes.byref(_mx(up, "up", n_experts * N, padded, dev))
     _call("moe_mx_grouped_gemm", dev, stream, ctypes.byref(xm), T, n_rows, ctypes.byref(wm), um, n_experts, N, K,
           _dense(offsets, "offsets", torch.int32, n_experts + 1, dev),
           _dense(row_tok, "row_tok", torch.int32, n_rows, dev), _dense(row_w, "row_w", torch.float32, n_rows, dev),
