@@ -90,44 +90,39 @@ MOE_DEV int swz(int R) {
 MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
 
 // Fills lo[e] (e = 0 .. E) with the groups' first rows, inside [0, n_rows]
-// whatever the offsets hold, and (PRE) pre[e] with the row tiles of the
-// groups before e, pre[E] = all of them.  Group e has max(lo[e + 1] - lo[e],
-// 0) rows.
-template <bool PRE, int NT>
-MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch) {
+// whatever the offsets hold, and pre[e] with the sum of weight(rows) over the
+// groups before e.  Group e has max(lo[e + 1] - lo[e], 0) rows.
+template <int NT, class Weight>
+MOE_DEV void group_table(const GroupedArgs &a, int *lo, int *pre, int *scratch, Weight weight) {
   const int tid = threadIdx.x, wave = tid >> 6;
-  int before = 0;  // row tiles of the experts of earlier passes
+  int before = 0;  // the sum over the experts of earlier passes
   for (int e0 = 0; e0 <= a.E; e0 += NT) {
     const int e = e0 + tid;
-    int first = 0, n = 0;
+    int first = 0, mine = 0;
     if (e <= a.E) {
       // without offsets E is 1
       first = a.offsets ? min(max(a.offsets[e], 0), a.n_rows) : e * a.n_rows;
-      if (e < a.E) n = max((a.offsets ? min(max(a.offsets[e + 1], 0), a.n_rows) : a.n_rows) - first, 0);
+      if (e < a.E) mine = weight(max((a.offsets ? min(max(a.offsets[e + 1], 0), a.n_rows) : a.n_rows) - first, 0));
       lo[e] = first;
     }
-    if constexpr (PRE) {
-      const int mine = (n + kGrRows - 1) / kGrRows;
-      const int upto = wave_scan(mine);
-      if (e0 > 0) lds_barrier();  // scratch has been read
-      if (lane_id() == 63) scratch[wave] = upto;
-      lds_barrier();
-      int base = before, all = 0;
+    const int upto = wave_scan(mine);
+    if (e0 > 0) lds_barrier();  // scratch has been read
+    if (lane_id() == 63) scratch[wave] = upto;
+    lds_barrier();
+    int base = before, all = 0;
 #pragma unroll
-      for (int w = 0; w < NT / 64; ++w) {
-        const int x = scratch[w];
-        base += w < wave ? x : 0;
-        all += x;
-      }
-      if (e <= a.E) pre[e] = base + upto - mine;
-      before += all;
+    for (int w = 0; w < NT / 64; ++w) {
+      const int x = scratch[w];
+      base += w < wave ? x : 0;
+      all += x;
     }
+    if (e <= a.E) pre[e] = base + upto - mine;
+    before += all;
   }
   lds_barrier();
 }
 
-// The expert of row tile j (pre[e] <= j < pre[e + 1]), found by the whole
-// wave: among every 16th entry, then among those 16.
+// The expert e with pre[e] <= j < pre[e + 1], found by the whole wave: among every 16th entry, then among those 16.
 MOE_DEV int tile_expert(const int *pre, int E, int j) {
   const int lane = lane_id();
   const int c = __popcll(__ballot(16 * lane < E && pre[16 * lane] <= j)) - 1;
@@ -145,11 +140,13 @@ struct Tile {
 
 template <int KIND, int TYPE, int OUT, int CT, int NW, int STAGES, bool SWIGLU>
 __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a, int32_t col_tiles, int32_t dw_tiles) {
-  // dw: group e's rows in a.splits parts, part p of it the `expert` p E + e
   constexpr int NT = 64 * NW;
   constexpr int kWaveRows = kGrRows * CT / 64 / NW;  // results of a wave: so many rows, 64 columns
   constexpr int BT = kGrRows;
   constexpr bool MX = KIND == kGroupedMx, DW = KIND == kGroupedDw;
+  // dw with few tiles: group e's rows in a.splits parts, part p of it the
+  // `expert` p E + e (grouped_dw_splits: at most kLoneTiles tiles)
+  constexpr bool PARTS = DW && CT == 128 && NW == 8;
   constexpr bool ACROSS_A = KIND == kGroupedDx || DW, ACROSS_B = DW;  // reduction across the operand's rows
   constexpr int NA = CT / 8 / NW, NB = BT / 8 / NW;                   // 1 KB requests a wave, a step
   constexpr int FB = kWaveRows / 16;                                  // 16-row fragments of a wave
@@ -185,14 +182,34 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
   const uint32_t token0 = __builtin_amdgcn_readfirstlane(lds_addr(row_token));
   const uint32_t scale0 = __builtin_amdgcn_readfirstlane(lds_addr(row_scale));
 
-  group_table<!DW, NT>(a, lo, pre, scratch);
-  const int n_items = DW ? a.splits * a.E * col_tiles * dw_tiles : __builtin_amdgcn_readfirstlane(pre[a.E]) * col_tiles;
-  // Blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items,
-  // its blocks in turn.  (Ranges of their own for 16, 8, 4 or 1 of the blocks
-  // lose the sharing in the L2: dw 606 -> 796, 784, 841, 1110 us.)
+  // pre: row tiles; dw: what a tile of the expert costs, in steps of its
+  // rows, its stores being worth one or two
+  group_table<NT>(a, lo, pre, scratch, [](int n) {
+    return DW ? (n + kGrRed - 1) / kGrRed + (OUT == MOE_T_F32 ? 2 : 1) : (n + kGrRows - 1) / kGrRows;
+  });
+  // Blocks go to the XCDs in turn: XCD x takes the x-th eighth of the items
+  // (dw, with half a step a group or more: of their costs; by their number the
+  // XCD with the longest groups is late: 16000 rows over 256 matrices of 1024
+  // x 2048, the longest group 500, 327 -> 302 us; with shorter groups finding
+  // them costs more: 640 rows over 64 of 512 x 1024 18.3 -> 19.4), its blocks
+  // in turn.  (Ranges of their own for 16, 8, 4 or 1
+  // of the blocks lose the sharing in the L2: dw 606 -> 796, 784, 841, 1110
+  // us.)
+  const int dw_items = col_tiles * dw_tiles;  // of an expert
+  const int n_items = DW ? (PARTS ? a.splits : 1) * a.E * dw_items : __builtin_amdgcn_readfirstlane(pre[a.E]) * col_tiles;
+  auto eighth = [&](int x) __attribute__((always_inline)) {
+    if (DW && !PARTS && x < 8 && a.n_rows > kGrRed / 2 * a.E) {
+      const int at = __builtin_amdgcn_readfirstlane(pre[a.E]) * x;  // in eighths
+      const int e = tile_expert(pre, a.E, at >> 3);
+      const int before = __builtin_amdgcn_readfirstlane(pre[e]), cost = __builtin_amdgcn_readfirstlane(pre[e + 1]) - before;
+      const float part = static_cast<float>(at - 8 * before) * __builtin_amdgcn_rcpf(8.f * static_cast<float>(cost));
+      const int in = static_cast<int>(part * static_cast<float>(dw_items));
+      return e * dw_items + min(__builtin_amdgcn_readfirstlane(in), dw_items);
+    }
+    return static_cast<int>(static_cast<int64_t>(n_items) * x / 8);
+  };
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
-  const int end = static_cast<int>(static_cast<int64_t>(n_items) * (xcd + 1) / 8);
-  const int begin = static_cast<int>(static_cast<int64_t>(n_items) * xcd / 8) + (blockIdx.x >> 3);
+  const int begin = eighth(xcd) + (blockIdx.x >> 3), end = eighth(xcd + 1);
   const int count = begin < end ? (end - begin + per - 1) / per : 0;  // this block's tiles
 
   // Places of tiles 32 c .. 32 c + 31 into the table's half c & 1, a wave a
@@ -208,18 +225,30 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
             make_int4(e | (item - j * col_tiles) << 10, j - pre[e], lo[e], max(lo[e + 1] - lo[e], 0));
     }
   };
-  auto locate = [&](int i) __attribute__((always_inline)) {
-    Tile t;
+  // Tile i of this block after tile i - 1 (in t): dw's by adding `per` items
+  // in experts, row and column tiles.
+  const int dw_e = DW ? per / dw_items : 0;
+  const int dw_b = DW ? per / col_tiles - dw_e * dw_tiles : 0, dw_c = DW ? per % col_tiles : 0;
+  auto locate = [&](Tile &t, int i) __attribute__((always_inline)) {
     if constexpr (DW) {
-      const int item = begin + i * per;
-      t.e = item / (col_tiles * dw_tiles);
-      const int in = item - t.e * (col_tiles * dw_tiles);
-      t.bt = in / col_tiles;
-      t.ct = in - t.bt * col_tiles;
-      const int part = t.e / a.E, e = t.e - part * a.E;
+      if (i == 0) {
+        const int row = begin / col_tiles;
+        t.ct = begin - row * col_tiles;
+        t.e = row / dw_tiles;
+        t.bt = row - t.e * dw_tiles;
+      } else {
+        t.ct += dw_c;
+        const int over_c = t.ct >= col_tiles;
+        t.ct -= over_c ? col_tiles : 0;
+        t.bt += dw_b + over_c;
+        const int over_b = t.bt >= dw_tiles;
+        t.bt -= over_b ? dw_tiles : 0;
+        t.e += dw_e + over_b;
+      }
+      const int part = PARTS ? t.e / a.E : 0, e = t.e - part * a.E;
       t.r0 = __builtin_amdgcn_readfirstlane(lo[e]);
       t.n = max(__builtin_amdgcn_readfirstlane(lo[e + 1]) - t.r0, 0);
-      if (a.splits > 1) {
+      if (PARTS && a.splits > 1) {
         const int rows = ((t.n + kGrRed - 1) / kGrRed + a.splits - 1) / a.splits * kGrRed;  // of a part
         t.r0 += min(part * rows, t.n);
         t.n = min(rows, max(t.n - part * rows, 0));
@@ -237,7 +266,6 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
     const int red = DW ? t.n : a.red;
     constexpr int kUnit = ACROSS_A ? kGrRed : kGrStep;
     t.steps = (red + kUnit - 1) / kUnit;
-    return t;
   };
 
   // ---- The requesting side runs kAhead steps before the products, across
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
   };
   auto settle = [&](Cursor &c) __attribute__((always_inline)) {  // on a tile with steps, or past the last
     while (c.i < count) {
-      c.t = locate(c.i);
+      locate(c.t, c.i);
       if (!DW || c.t.steps > 0) break;
       ++c.i;
     }
@@ -496,6 +524,7 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
   }
   int done_slot = 0;   // of row_scale
   int scale_read = 0;  // of `scales`
+  Tile t{};
   for (int i = 0; i < count; ++i) {
     if constexpr (!DW) {
       // the next half of the table, once every wave has left the one it takes
@@ -505,7 +534,7 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
         lds_barrier();
       }
     }
-    const Tile t = locate(i);
+    locate(t, i);
     f32x4_t acc[4][FB];
 #pragma unroll
     for (int f = 0; f < 4; ++f)
@@ -670,7 +699,7 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
   const TileCount n(a, SWIGLU ? CT / 2 : CT);
   constexpr int64_t kMost = NW == 4 ? 512 : 256;  // blocks that the compute units hold
   const int64_t blocks = (n.tiles * (KIND == kGroupedDw ? a.splits : 1) + 7) / 8 * 8;
-  const uint32_t lds = (a.E + 1) * sizeof(int) * (KIND == kGroupedDw ? 1 : 2);
+  const uint32_t lds = 2 * (a.E + 1) * sizeof(int);
   grouped_tile_kernel<KIND, TYPE, OUT, CT, NW, STAGES, SWIGLU>
       <<<dim3(static_cast<uint32_t>(blocks < kMost ? blocks : kMost)), 64 * NW, lds, s>>>(a, n.col_tiles, n.dw_tiles);
   return hipGetLastError();
@@ -683,8 +712,12 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
 // over 256 experts of 1024 x 2048 342 against 403 us and 520 against 602, fwd
 // of 32768 rows 275 against 297, dx 278 against 297; below it the narrow one:
 // 512 rows over eight experts of 2048 x 2048 fwd 29.0 against 34.7, dw of one
-// expert 106 against 139.  MXFP4's scales leave the wide tile no third buffer,
-// and with two it loses (gate/up of 16384 rows 91 against 80 us).
+// expert 106 against 139.  dw asks for eight a compute unit (much of a tile is
+// its stores, and two blocks overlap them): 4001 rows over 64 matrices of 520 x
+// 1000 (1280 wide tiles) 29 us wide, 26 narrow, of 512 x 1024 (1024) 24 and 22;
+// over 100 of 520 x 1504 (3000) 55 wide, 62 narrow.  MXFP4's scales leave the
+// wide tile no third buffer, and with two it loses (gate/up of 16384 rows 91
+// against 80 us).
 //
 // With at most one tile a compute unit the narrow tile gets a block of eight
 // waves of 64 x 32 results and three buffers: half the requests and products
@@ -692,12 +725,13 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
 // -> 12.7 us, MXFP4 8.0 -> 7.2, dw of 16384 rows and one 2048 x 2048 matrix 257
 // -> 188); with more tiles two blocks of four waves are better (4096 rows over
 // eight experts 20.7 against 27.4).
-constexpr int64_t kWideTiles = 1024, kLoneTiles = 256;
+constexpr int64_t kWideTiles = 1024, kWideTilesDw = 2048, kLoneTiles = 256;
 
 template <int KIND, int TYPE, int OUT>
 hipError_t launch_width(const GroupedArgs &a, hipStream_t s) {
   const int64_t parts = KIND == kGroupedDw ? a.splits : 1;
-  if (TileCount(a, 256).tiles * parts >= kWideTiles) return launch_tile<KIND, TYPE, OUT, 256, 8, 3, false>(a, s);
+  if (TileCount(a, 256).tiles >= (KIND == kGroupedDw ? kWideTilesDw : kWideTiles))
+    return launch_tile<KIND, TYPE, OUT, 256, 8, 3, false>(a, s);
   return TileCount(a, 128).tiles * parts <= kLoneTiles ? launch_tile<KIND, TYPE, OUT, 128, 8, 3, false>(a, s)
                                                        : launch_tile<KIND, TYPE, OUT, 128, 4, 2, false>(a, s);
 }

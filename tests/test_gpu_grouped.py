@@ -263,6 +263,27 @@ def test_grouped_gemm_dw_in_parts(mb, counts, N, K, dtype, out_dtype):
         assert torch.equal(out, first) and bool((ws[need:] == 0xFF).all())
 
 
+@pytest.mark.parametrize("E,N,K,dtype,out_dtype", [(12, 520, 1000, BF, BF), (33, 1032, 1800, HF, HF)])
+@pytest.mark.parametrize("heavy", [0, -1])
+def test_grouped_gemm_dw_uneven_groups(mb, E, N, K, dtype, out_dtype, heavy):
+    """One group with most of the rows, first or last, empty ones and short ones: every tile is made, by one block."""
+    counts = [0 if e % 3 == 1 else 5 + e for e in range(E)]
+    counts[heavy] = 1500
+    off = torch.tensor([3] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+    n_rows = int(off[-1]) + 2
+    say(f"dw uneven E={E} N={N} K={K} {dtype} heavy={heavy}")
+    g = torch.Generator().manual_seed(E + heavy)
+    dy, x = torch.randn(n_rows, N, generator=g).to(dtype), torch.randn(n_rows, K, generator=g).to(dtype)
+    out = torch.full((E, N, K), 7.0, dtype=out_dtype, device="cuda")
+    mb.grouped_gemm_dw(dev(dy), dev(x), dev(off), out)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        p, q = dy[a:b].double(), x[a:b].double()
+        ref = p.T @ q
+        limit = gu.rounded(ref, gu.sum_bound(p.abs().T @ q.abs(), max(1, b - a), 32), out_dtype)
+        assert bool(((out[e].cpu().double() - ref).abs() <= limit).all()), e
+
+
 def test_grouped_gemm_dw_without_rows_is_zero(mb):
     say("dw, n_rows = 0")
     out = torch.full((3, 16, 24), 7.0, device="cuda")
