@@ -12,9 +12,20 @@
 //
 // Both kernels do a handful of operations a byte and are bound by HBM.  A
 // row's 128 elements (the padding unit) belong to 16 lanes of eight elements:
-// a lane's 16-bit input is one 16-byte load, its codes one 4-byte word, four
-// lanes share a block, and one lane in 16 writes the unit's four scale bytes
-// as a word.
+// a lane's 16-bit values are one 16-byte access, its codes one 4-byte word,
+// four lanes share a block, and one lane in 16 writes the unit's four scale
+// bytes as a word.  Rows begin at any element: 16-byte accesses need no more
+// alignment than that here, so that only the end of a row differs (131072 rows
+// of 1999 bf16 in 156 us and back in 157; element by element 283 and 405).
+//
+// Codes to fp32 go by 32 lanes of four elements, so that a store is 1 KB in
+// one piece (131072 x 2048: 290 us for 341); results go past the caches: they
+// outgrow them, and the way to HBM is shorter (229 us, bf16 111 for 139).
+// Rates at 131072 x 2048: from bf16 5.0 TB/s, fp32 4.8; to bf16 6.1, fp32 5.3.
+// (Loads past the caches help from bf16, 136 -> 123 us, and hurt from fp32 rows
+// of odd length, 251 -> 280.)
+#include <type_traits>
+
 #include "grouped.h"
 
 namespace moe {
@@ -22,8 +33,11 @@ namespace moe {
 namespace {
 
 constexpr int kMxThreads = 256;
-constexpr int kMxUnits = kMxThreads / 16;  // 128-element units a block works on at a time
 constexpr int kMxMaxBlocks = 256 * 16;
+// lanes to a 128-element unit
+constexpr int kQuantLanes = 16;
+template <int TYPE>
+constexpr int kDequantLanes = TYPE == MOE_T_F32 ? 32 : 16;
 
 // Unit u, u + stride, ... of a row-major array of `upr` units a row, without
 // a division a step.
@@ -44,6 +58,18 @@ struct UnitWalk {
       ++row;
     }
   }
+};
+
+// sixteen bytes at any element of the size
+template <int SIZE>
+struct Piece;
+template <>
+struct Piece<2> {
+  typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Piece<4> {
+  typedef uint32_t T __attribute__((ext_vector_type(4), aligned(4)));
 };
 
 template <int TYPE>
@@ -67,27 +93,31 @@ struct Elem<MOE_T_F32> {
   static MOE_DEV T put(float v) { return v; }
 };
 
-// Eight elements from column c of a row; VEC: the row is whole 16-byte pieces
-// there.  Columns past the end are zeros.
-template <int TYPE, bool VEC>
+// Eight elements from column c of a row; columns past the end are zeros.  A
+// lane at the row's end loads its last eight and moves them down: eight loads
+// of one element each took 131072 rows of 1999 bf16 from 153 to 213 us.
+template <int TYPE>
 MOE_DEV void load8(const typename Elem<TYPE>::T *row, int c, int cols, float (&v)[8]) {
   using E = Elem<TYPE>;
-  if constexpr (VEC) {
-    if (c < cols) {
-      typename E::T t[8];
-      constexpr int kPieces = sizeof(t) / 16;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        reinterpret_cast<uint4 *>(t)[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (c >= cols) return;
+  if (cols < 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = E::get(t[i]);
-    } else {
+    for (int i = 0; i < 8; ++i)
+      if (i < cols) v[i] = E::get(row[i]);
+    return;
+  }
+  const int at = min(c, cols - 8), down = c - at;
+  typename E::T t[8];
+  __builtin_memcpy(t, row + at, sizeof(t));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) v[i] = E::get(t[i]);
+  if (__ballot(down != 0) == 0) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? E::get(row[c + i]) : 0.f;
+  for (int by = 4; by > 0; by >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = down & by ? (i + by < 8 ? v[i + by] : 0.f) : v[i];
   }
 }
 
@@ -98,16 +128,17 @@ MOE_DEV uint32_t dpp_u32_xor2(uint32_t v) {
   return __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, true);
 }
 
-template <int TYPE, bool VEC>
+template <int TYPE>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(MxQuantArgs a, int32_t upr, int64_t units) {
   using E = Elem<TYPE>;
+  constexpr int kUnits = kMxThreads / kQuantLanes;
   const int lane16 = threadIdx.x & 15;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kMxUnits + (threadIdx.x >> 4);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kMxUnits;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kUnits + (threadIdx.x >> 4);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kUnits;
   UnitWalk w(first, stride, upr);
   for (int64_t u = first; u < units; u += stride, w.next()) {
     float v[8];
-    load8<TYPE, VEC>(static_cast<const typename E::T *>(a.x) + w.row * a.x_ld, w.unit * kMxPad + lane16 * 8, a.cols, v);
+    load8<TYPE>(static_cast<const typename E::T *>(a.x) + w.row * a.x_ld, w.unit * kMxPad + lane16 * 8, a.cols, v);
     // magnitudes compare as their bits; infinities and NaN are above all others
     uint32_t m = 0;
 #pragma unroll
@@ -131,82 +162,82 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(MxQuantArgs a, 
   }
 }
 
-template <int TYPE, bool VEC>
+template <int TYPE>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(MxDequantArgs a, int32_t upr, int64_t units) {
   using E = Elem<TYPE>;
-  const int lane16 = threadIdx.x & 15;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kMxUnits + (threadIdx.x >> 4);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kMxUnits;
+  constexpr int kLanes = kDequantLanes<TYPE>, kUnits = kMxThreads / kLanes, N = kMxPad / kLanes;  // elements a lane
+  using Codes = std::conditional_t<N == 8, uint32_t, uint16_t>;
+  const int in = threadIdx.x & (kLanes - 1);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kUnits + threadIdx.x / kLanes;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kUnits;
   UnitWalk w(first, stride, upr);
   for (int64_t u = first; u < units; u += stride, w.next()) {
     const size_t at = static_cast<size_t>(w.row) * upr + w.unit;
-    const uint32_t q = reinterpret_cast<const uint32_t *>(a.q)[at * 16 + lane16];
-    const uint32_t code = a.s[at * 4 + (lane16 >> 2)];
+    const uint32_t q = reinterpret_cast<const Codes *>(a.q)[at * kLanes + in];
+    const uint32_t code = a.s[at * 4 + in / (kLanes / 4)];
     const float scale = __uint_as_float(code == 255u ? 0x7FC00000u : code == 0 ? 0x00400000u : code << 23);
     f32x2_t p[4];
     p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
     p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
     p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
     p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
-    typename E::T t[8];
+    typename E::T t[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = E::put(p[i >> 1][i & 1] * scale);
+    for (int i = 0; i < N; ++i) t[i] = E::put(p[i >> 1][i & 1] * scale);
     typename E::T *row = static_cast<typename E::T *>(a.out) + w.row * a.out_ld;
-    const int c = w.unit * kMxPad + lane16 * 8;
-    if constexpr (VEC) {
-      if (c < a.cols) {
-        constexpr int kPieces = sizeof(t) / 16;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          reinterpret_cast<uint4 *>(row + c)[i] = reinterpret_cast<const uint4 *>(t)[i];
+    const int c = w.unit * kMxPad + in * N;
+    if (c + N <= a.cols) {
+      using P = typename Piece<sizeof(t[0])>::T;
+      P whole;
+      __builtin_memcpy(&whole, t, sizeof(t));
+      // past the caches (see above), but for a row's part of a unit, whose
+      // lines the next row may share
+      if (w.unit * kMxPad + kMxPad <= a.cols) {
+        __builtin_nontemporal_store(whole, reinterpret_cast<P *>(row + c));
+      } else {
+        __asm__ volatile("" ::: "memory");  // else the compiler makes one plain store of both
+        *reinterpret_cast<P *>(row + c) = whole;
+        __asm__ volatile("" ::: "memory");
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < N; ++i)
         if (c + i < a.cols) row[c + i] = t[i];
     }
   }
 }
 
-// whole eight-element pieces everywhere: 16-byte requests
-bool vec_ok(const void *p, int64_t ld, int32_t cols, int32_t type) {
-  const int64_t size = type == MOE_T_F32 ? 4 : 2;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * size) % 16 == 0 && cols % 8 == 0;
-}
-
 template <class Args, class K>
-hipError_t launch_units(const Args &a, K vec, K scalar, bool use_vec, hipStream_t s) {
+hipError_t launch_units(const Args &a, K kernel, int lanes, hipStream_t s) {
   const int32_t upr = (a.cols + kMxPad - 1) / kMxPad;
   const int64_t units = static_cast<int64_t>(a.rows) * upr;
-  const int64_t blocks = (units + kMxUnits - 1) / kMxUnits;
+  const int64_t blocks = (units * lanes + kMxThreads - 1) / kMxThreads;
   const dim3 grid(static_cast<uint32_t>(blocks < kMxMaxBlocks ? blocks : kMxMaxBlocks));
-  (use_vec ? vec : scalar)<<<grid, kMxThreads, 0, s>>>(a, upr, units);
+  kernel<<<grid, kMxThreads, 0, s>>>(a, upr, units);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t s) {
-  const bool v = vec_ok(a.x, a.x_ld, a.cols, a.type);
   switch (a.type) {
     case MOE_T_BF16:
-      return launch_units(a, mx_quantize_kernel<MOE_T_BF16, true>, mx_quantize_kernel<MOE_T_BF16, false>, v, s);
+      return launch_units(a, mx_quantize_kernel<MOE_T_BF16>, kQuantLanes, s);
     case MOE_T_F16:
-      return launch_units(a, mx_quantize_kernel<MOE_T_F16, true>, mx_quantize_kernel<MOE_T_F16, false>, v, s);
+      return launch_units(a, mx_quantize_kernel<MOE_T_F16>, kQuantLanes, s);
     default:
-      return launch_units(a, mx_quantize_kernel<MOE_T_F32, true>, mx_quantize_kernel<MOE_T_F32, false>, v, s);
+      return launch_units(a, mx_quantize_kernel<MOE_T_F32>, kQuantLanes, s);
   }
 }
 
 hipError_t launch_mx_dequantize(const MxDequantArgs &a, hipStream_t s) {
-  const bool v = vec_ok(a.out, a.out_ld, a.cols, a.type);
   switch (a.type) {
     case MOE_T_BF16:
-      return launch_units(a, mx_dequantize_kernel<MOE_T_BF16, true>, mx_dequantize_kernel<MOE_T_BF16, false>, v, s);
+      return launch_units(a, mx_dequantize_kernel<MOE_T_BF16>, kDequantLanes<MOE_T_BF16>, s);
     case MOE_T_F16:
-      return launch_units(a, mx_dequantize_kernel<MOE_T_F16, true>, mx_dequantize_kernel<MOE_T_F16, false>, v, s);
+      return launch_units(a, mx_dequantize_kernel<MOE_T_F16>, kDequantLanes<MOE_T_F16>, s);
     default:
-      return launch_units(a, mx_dequantize_kernel<MOE_T_F32, true>, mx_dequantize_kernel<MOE_T_F32, false>, v, s);
+      return launch_units(a, mx_dequantize_kernel<MOE_T_F32>, kDequantLanes<MOE_T_F32>, s);
   }
 }
 

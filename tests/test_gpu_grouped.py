@@ -66,6 +66,28 @@ def test_mx_quantize_bits(mb, dtype, rows, cols, pad):
             assert bool((out.as_strided((rows, pad), (cols + pad, 1), cols) == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_mx_rows_at_any_element(mb, dtype):
+    """Rows that begin at any element, of every length beside a unit's and a lane's end, in every phase of 16 bytes."""
+    say(f"rows at any element {dtype}")
+    g = torch.Generator().manual_seed(11)
+    for cols in (1, 2, 5, 7, 8, 9, 15, 17, 31, 63, 65, 127, 129, 135, 137, 257):
+        for first in (1, 2, 3):
+            ld = cols + first
+            x = torch.randn(6, cols, generator=g).to(dtype)
+            base = torch.full((first + 6 * ld,), float("nan"), dtype=dtype, device="cuda")
+            rows = base.as_strided((6, cols), (ld, 1), first)
+            rows.copy_(x)
+            got = encode(mb, rows)
+            same_codes(got, gu.mx_encode(x.float()))
+            base.fill_(7.0)
+            mb.mx_dequantize(*got, rows)
+            assert torch.equal(rows.cpu(), gu.mx_decode(got[0].cpu(), got[1].cpu(), cols).to(dtype))
+            left = torch.ones(base.numel(), dtype=torch.bool)
+            left.as_strided((6, cols), (ld, 1), first).fill_(False)
+            assert bool((base.cpu()[left] == 7.0).all())
+
+
 def test_mx_quantize_every_16_bit_value(mb):
     """Every finite bfloat16 and float16 value as a block's largest and beside larger ones, and the borders of the grid
     at both ends of fp32's range."""
