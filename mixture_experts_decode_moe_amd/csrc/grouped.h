@@ -46,7 +46,6 @@ struct GroupedArgs {
   const float *row_w;
   char *out;
   int64_t out_ld;        // elements
-  int32_t out_vec;       // out rows are 16-byte aligned
   int32_t splits;        // dw: parts of a group's rows (1: none)
   char *parts;           // dw with parts: float [splits][E][nb][na]
 };

@@ -71,7 +71,6 @@ GroupedArgs grouped_args(int32_t kind, int32_t type, int32_t out_type, int32_t T
   a.out = static_cast<char *>(out);
   a.out_ld = out_ld;
   a.splits = 1;
-  a.out_vec = aligned(out, 16) && (out_ld * type_size(out_type)) % 16 == 0;
   return a;
 }
 

@@ -80,14 +80,11 @@ struct Packed {
   template <bool WHOLE>
   MOE_DEV void store(const GroupedArgs &a, int64_t at, int col) const {
     char *o = a.out + (at + col) * (OUT == MOE_T_F32 ? 4 : 2);
-    if (WHOLE || (a.out_vec && col + kCols <= a.na)) {
+    if (WHOLE || col + kCols <= a.na) {
       // through the caches: stores past them (nontemporal) halve dw's rate
       // where there is little to read (512 rows over 256 experts of 1024 x
       // 2048: 342 against 565 us; 32768 rows: 520 against 603)
-      if constexpr (W == 4)
-        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-      else
-        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+      __builtin_memcpy(o, w, sizeof(w));  // at any element
     } else {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {

@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
         }
       }
     };
-    if (a.out_vec && (t.ct + 1) * kCols <= a.na) {
+    if ((t.ct + 1) * kCols <= a.na) {
       store_tile(IntC<1>{});
       if (t.b_rows >= BT) {  // none of the stores was skipped
 #pragma unroll
@@ -796,7 +796,6 @@ hipError_t launch_dw_split(const GroupedArgs &a, hipStream_t s) {
   GroupedArgs p = a;
   p.out = a.parts;
   p.out_type = MOE_T_F32;
-  p.out_vec = 1;
   hipError_t e = launch_16bit<kGroupedDw>(p, s);
   if (e != hipSuccess) return e;
   const int64_t n4 = static_cast<int64_t>(a.E) * a.nb * a.na / 4;
