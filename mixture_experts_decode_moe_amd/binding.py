@@ -6,6 +6,7 @@ kernels.  Importing this module fails loudly if the library is not built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -475,9 +476,8 @@ def grouped_gemm_dw(dy: torch.Tensor, x: torch.Tensor, offsets, dw: torch.Tensor
         raise ValueError("dy [n_rows][N], x [T][K] (of one type) and dw [E][N][K] do not fit")
     need = _lib.moe_grouped_gemm_dw_workspace_bytes(n_rows, E, N, K)
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
-        if stream is not None:
-            ws.record_stream(stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # of the memory that `stream` uses
+            ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
     wp = _dense(ws, "ws", torch.uint8, need, dev)
     _call("moe_grouped_gemm_dw", dev, stream, yp, y_ld, xp, x_ld, T, n_rows, kind, E, N, K,
           _dense(offsets, "offsets", torch.int32, E + 1, dev), _dense(row_tok, "row_tok", torch.int32, n_rows, dev),

@@ -670,6 +670,57 @@ def test_expert_training_step(mb, dtype):
     assert abs(slope - float(dtok[i, j])) <= err
 
 
+def test_gradients_captured_and_on_two_streams(mb):
+    """Forward, dx and a dw in parts (whose workspace the binding allocates) in one graph, replayed between eager calls,
+    and at once on two streams: the eager bits each time."""
+    say("gradients: graph and streams")
+    g = torch.Generator().manual_seed(8)
+    off = torch.tensor([0, 1500, 1500, 4000], dtype=torch.int32).cuda()
+    sets = []
+    for _ in range(2):
+        x, dy = torch.randn(4000, 264, generator=g).to(BF).cuda(), torch.randn(4000, 136, generator=g).to(BF).cuda()
+        w = torch.randn(3, 136, 264, generator=g).to(BF).cuda()
+        sets.append((x, dy, w, torch.empty(4000, 136, device="cuda"), torch.empty(4000, 264, device="cuda"),
+                     torch.empty(3, 136, 264, device="cuda")))
+    assert mb.grouped_gemm_dw_workspace_bytes(4000, 3, 136, 264) > 0
+
+    def step(k, stream=None):
+        x, dy, w, y, dx, dw = sets[k]
+        mb.grouped_gemm(x, w, off, y, stream=stream)
+        mb.grouped_gemm_dx(dy, w, off, dx, stream=stream)
+        mb.grouped_gemm_dw(dy, x, off, dw, stream=stream)
+
+    def results(k):
+        return [t.clone() for t in sets[k][3:]]
+
+    eager = []
+    for k in (0, 1):
+        step(k)
+        eager.append(results(k))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    for _ in range(3):
+        for t in sets[0][3:]:
+            t.zero_()
+        graph.replay()
+        step(1)
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(results(k), eager[k]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for t in sets[0][3:] + sets[1][3:]:
+        t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k in (0, 1):
+            step(k, streams[k])
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(results(k), eager[k]))
+
+
 def test_two_calls_on_two_streams(mb):
     """Calls share nothing: two at once on two streams give what they give alone."""
     say("two streams at once")
