@@ -1,5 +1,5 @@
 // Products grouped by expert: 16-bit rows and matrices with both gradients,
-// and MXFP4 rows and matrices, on 128-column tiles of the matrix cores.
+// and MXFP4 rows and matrices, on tiles of the matrix cores.
 //
 //   fwd  out[r][n]   = sum_k x[r][k]  w_e[n][k]
 //   dx   dx[r][k]    = sum_n dy[r][n] w_e[n][k]
@@ -20,14 +20,14 @@
 // transposing load (ds_read_b64_tr_b16: 16 lanes take a 4 x 16 patch and get
 // a column of four each).
 //
-// Staging is direct loads into LDS (no registers), one or two steps ahead.
+// Staging is direct loads into LDS (no registers), one to five steps ahead.
 // What lies past the end of the reduction reads a page of zeros, so that tails
 // need no masks in the product and never meet another group's NaN.  The pieces
 // of a row are permuted by an XOR with row bits so that operand reads meet the
 // banks equally.
 //
-// A block loops over tiles (expert, 128 rows, 128 or 256 columns); a wave has
-// 64 x 64 results.  The column tiles of a row tile follow one another and each
+// A block loops over tiles (expert, 128 rows, 64 to 256 columns); a wave has up
+// to 64 x 64 results.  The column tiles of a row tile follow one another and each
 // XCD works on its own range of them, so that a group's rows and an expert's
 // matrix are shared in its L2.
 //
@@ -86,8 +86,12 @@ template <bool PAIRS>
 MOE_DEV int swz(int R) {
   return PAIRS ? ((R >> 1) & 1) | (((R >> 3) & 3) << 1) : (R >> 1) & 7;
 }
-// the same for transposed reads: eight rows of a half wave read 32 bytes each
-MOE_DEV int swz_t(int R) { return ((R & 3) | (((R >> 3) & 1) << 2)) << 1; }
+// the same for transposed reads of rows of COLS columns: eight rows of a half
+// wave read 32 bytes each
+template <int COLS>
+MOE_DEV int swz_t(int R) {
+  return ((R & 3) | (((R >> 3) & 1) << 2)) << 1 & (COLS / 8 - 1);
+}
 
 // Fills lo[e] (e = 0 .. E) with the groups' first rows, inside [0, n_rows]
 // whatever the offsets hold, and pre[e] with the sum of weight(rows) over the
@@ -330,14 +334,14 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
   };
   auto a_piece = [&](int i) __attribute__((always_inline)) {
     const int R = a_row(i);
-    return ACROSS_A ? (lane % (64 / kRowsA)) ^ swz_t(R) : (lane & 7) ^ swz<kPairs>(R);
+    return ACROSS_A ? (lane % (64 / kRowsA)) ^ swz_t<CT>(R) : (lane & 7) ^ swz<kPairs>(R);
   };
   auto b_row = [&](int i) __attribute__((always_inline)) {
     return ACROSS_B ? kRowsB * (wave + NW * i) + g : 8 * (wave + NW * i) + (lane >> 3);
   };
   auto b_piece = [&](int i) __attribute__((always_inline)) {
     const int R = b_row(i);
-    return ACROSS_B ? l16 ^ swz_t(R) : (lane & 7) ^ swz<false>(R);
+    return ACROSS_B ? l16 ^ swz_t<BT>(R) : (lane & 7) ^ swz<false>(R);
   };
   // addresses of the tile's first requests
   auto set_up = [&]() __attribute__((always_inline)) {
@@ -543,12 +547,13 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
 
     const int fragments = (t.b_rows - wb * kWaveRows + 15) >> 4;  // of this wave that have rows, or more than FB
     for (int s = 0; s < t.steps; ++s) {
-      if (after[0] >= kRequests + kStores)
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(kRequests + kStores));
-      else if (after[0] >= (kRequests > kStores ? kRequests : kStores))
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kRequests > kStores ? kRequests : kStores)));
-      else if (after[0] >= (kRequests < kStores ? kRequests : kStores))
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kRequests < kStores ? kRequests : kStores)));
+      constexpr int kLater = (kAhead - 1) * kRequests;  // requests of the later steps on their way
+      if (after[0] >= kLater + kStores)
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLater + kStores));
+      else if (after[0] >= (kLater > kStores ? kLater : kStores))
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kLater > kStores ? kLater : kStores)));
+      else if (after[0] >= (kLater < kStores ? kLater : kStores))
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm((kLater < kStores ? kLater : kStores)));
       else
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
       lds_barrier();  // every wave's part has landed, and the buffer before is free
@@ -575,13 +580,14 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
           // a fragment of columns from `col` on, of staged rows 32 kk + 8 g ..
           // + 7: 16 lanes give four rows' chunks of four columns, the chunk c
           // = 0..3 of a row at columns 4 c, or (pair >= 0) 8 c + 4 pair
-          auto across = [&](const char *t, int row_bytes, int col, int pair) __attribute__((always_inline)) {
+          auto across = [&](const char *t, auto cols_t, int col, int pair) __attribute__((always_inline)) {
+            constexpr int kTileCols = decltype(cols_t)::value;
             u32x4_t r;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int R = 32 * kk + 8 * g + 4 * j + (l16 >> 2);
-              const int piece = (col / 8 + (pair < 0 ? (l16 >> 1) & 1 : l16 & 3)) ^ swz_t(R);
-              const char *p = t + R * row_bytes + 16 * piece + 8 * (pair < 0 ? l16 & 1 : pair);
+              const int piece = (col / 8 + (pair < 0 ? (l16 >> 1) & 1 : l16 & 3)) ^ swz_t<kTileCols>(R);
+              const char *p = t + R * 2 * kTileCols + 16 * piece + 8 * (pair < 0 ? l16 & 1 : pair);
               const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                   (__attribute__((address_space(3))) s16x4_t *)(const_cast<char *>(p)));
               const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
@@ -593,8 +599,8 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             if constexpr (ACROSS_A) {
-              A[f] = kPairs ? across(ta, 2 * CT, 64 * wa + 32 * (f >> 1), f & 1)
-                            : across(ta, 2 * CT, 64 * wa + 16 * f, -1);
+              A[f] = kPairs ? across(ta, IntC<CT>{}, 64 * wa + 32 * (f >> 1), f & 1)
+                            : across(ta, IntC<CT>{}, 64 * wa + 16 * f, -1);
             } else {
               const int R =
                   64 * wa + (kPairs ? 32 * (f >> 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3) : 16 * f + l16);
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(64 * NW, 2) grouped_tile_kernel(GroupedArgs a,
           for (int h = 0; h < NF; ++h) {
             const int R = wb * kWaveRows + 16 * h + l16;
             if constexpr (ACROSS_B) {
-              B[h] = across(tb, 2 * BT, wb * kWaveRows + 16 * h, -1);
+              B[h] = across(tb, IntC<BT>{}, wb * kWaveRows + 16 * h, -1);
             } else {
               B[h] = along(tb, R, swz<false>(R));
               if constexpr (MX) sb[h] = *reinterpret_cast<const uint32_t *>(ts + 16 * (CT + R) + 4 * kk) >> (8 * g);
@@ -719,12 +725,14 @@ hipError_t launch_tile(const GroupedArgs &a, hipStream_t s) {
 // wide tile no third buffer, and with two it loses (gate/up of 16384 rows 91
 // against 80 us).
 //
-// With at most one tile a compute unit the narrow tile gets a block of eight
-// waves of 64 x 32 results and three buffers: half the requests and products
-// a wave in each step (fwd of 300 rows over eight experts of 1024 x 1024 15.7
-// -> 12.7 us, MXFP4 8.0 -> 7.2, dw of 16384 rows and one 2048 x 2048 matrix 257
-// -> 188); with more tiles two blocks of four waves are better (4096 rows over
-// eight experts 20.7 against 27.4).
+// With at most one tile a compute unit a tile's walk is the whole time, and a
+// block has eight waves: of 64 x 32 results in a 128-column tile with three
+// buffers (dw of 16384 rows and one 2048 x 2048 matrix 257 -> 188 us), or of 64
+// x 16 in a 64-column tile with six (MXFP4: five), where those are at most one a
+// compute unit too: 300 rows and one 2048 x 2048 matrix 24.7 -> 20.8 us, MXFP4
+// 10.9 -> 9.6, over eight of 1024 x 1024 12.7 -> 11.2 and 7.1 -> 6.4.  With
+// more tiles two blocks of four waves are better (4096 rows over those eight
+// 20.7 against 27.4).
 constexpr int64_t kWideTiles = 1024, kWideTilesDw = 2048, kLoneTiles = 256;
 
 template <int KIND, int TYPE, int OUT>
@@ -732,6 +740,9 @@ hipError_t launch_width(const GroupedArgs &a, hipStream_t s) {
   const int64_t parts = KIND == kGroupedDw ? a.splits : 1;
   if (TileCount(a, 256).tiles >= (KIND == kGroupedDw ? kWideTilesDw : kWideTiles))
     return launch_tile<KIND, TYPE, OUT, 256, 8, 3, false>(a, s);
+  if constexpr (KIND != kGroupedDw) {
+    if (TileCount(a, 64).tiles <= kLoneTiles) return launch_tile<KIND, TYPE, OUT, 64, 8, 6, false>(a, s);
+  }
   return TileCount(a, 128).tiles * parts <= kLoneTiles ? launch_tile<KIND, TYPE, OUT, 128, 8, 3, false>(a, s)
                                                        : launch_tile<KIND, TYPE, OUT, 128, 4, 2, false>(a, s);
 }
@@ -747,8 +758,10 @@ hipError_t launch_16bit(const GroupedArgs &a, hipStream_t s) {
 
 template <int OUT, bool SWIGLU>
 hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
-  return TileCount(a, SWIGLU ? 64 : 128).tiles <= kLoneTiles ? launch_tile<kGroupedMx, 0, OUT, 128, 8, 3, SWIGLU>(a, s)
-                                                             : launch_tile<kGroupedMx, 0, OUT, 128, 4, 2, SWIGLU>(a, s);
+  constexpr int kMats = SWIGLU ? 2 : 1;  // share a tile's columns
+  if (TileCount(a, 64 / kMats).tiles <= kLoneTiles) return launch_tile<kGroupedMx, 0, OUT, 64, 8, 5, SWIGLU>(a, s);
+  return TileCount(a, 128 / kMats).tiles <= kLoneTiles ? launch_tile<kGroupedMx, 0, OUT, 128, 8, 3, SWIGLU>(a, s)
+                                                       : launch_tile<kGroupedMx, 0, OUT, 128, 4, 2, SWIGLU>(a, s);
 }
 
 template <int OUT>
@@ -757,19 +770,17 @@ hipError_t launch_mx(const GroupedArgs &a, hipStream_t s) {
 }
 
 // Whether the few-row kernel takes the call: its blocks, times the matrices of
-// one, are at most five a compute unit in 16 bits, four in MXFP4.  It spreads a
-// call over the chip where tiles leave most of it idle, and its time grows with
-// its blocks; the tiles' is that of one tile's steps until they fill the chip.
-// Both grow alike with the reduction's length.  Few rows against tiles, in us:
-// 16 bits, 2048 x 2048: 64 rows (640 blocks) 11.2 / 19.7, 128 rows (1152)
-// 19.0 / 24.3, 256 rows (2176) 34.7 / 24.4; 512 x 2048: 512 rows (1056)
-// 19.1 / 24.2; sixteen of 512 x 512: 512 rows (1536) 8.5 / 8.3; eight of 256 x
-// 8192: 1024 rows (1152) 80 / 84.  MXFP4: 10.5 / 10.8, 18.0 / 10.9 and
-// 10.3 / 10.7 for 1152, 2176 and 1056; with SwiGLU 9.1 / 10.0 and 14.3 / 11.3
-// for 640 and 1152, 8.9 / 10.0 for 384 blocks of four experts.
+// one, are at most four a compute unit.  It spreads a call over the chip where
+// tiles leave most of it idle, and its time grows with its blocks; the tiles'
+// is that of one tile's steps until they fill the chip.  Both grow alike with
+// the reduction's length.  Few rows against tiles, in us: 16 bits, 2048 x 2048:
+// 64 rows (640 blocks) 11.0 / 17.9, 128 rows (1152) 18.6 / 20.2, 256 rows (2176)
+// 34.5 / 20.6; four of 512 x 2048: 128 rows (384) 10.8 / 17.6, 512 rows (1152)
+// 22.6 / 20.5.  MXFP4 the same: 6.5 / 8.5, 10.1 / 9.3, 17.8 / 9.5, 6.3 / 8.4 and
+// 11.5 / 9.4; with SwiGLU 8.5 / 9.0 for 384 blocks, 8.8 / 9.1 for 640.
 bool few_rows(const GroupedArgs &a) {
   if (a.kind != kGroupedFwd && a.kind != kGroupedMx) return false;
-  return grouped_few_blocks(a) * (a.a2 ? 2 : 1) <= (a.kind == kGroupedMx ? 4 : 5) * 256;
+  return grouped_few_blocks(a) * (a.a2 ? 2 : 1) <= 4 * 256;
 }
 
 // dw[i] = the sum of its parts, in order
