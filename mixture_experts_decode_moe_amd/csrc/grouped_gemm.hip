@@ -33,8 +33,8 @@
 //
 // What bounds it: at the sizes of a layer every product is a stream of the
 // matrices and the results through HBM (wide tiles 4.5 to 5.0 TB/s of reads
-// with the rows beside them, dw 4.3 TB/s mostly of stores); a single 2048 x
-// 2048 matrix with 32768 rows reaches 960 TFLOP/s in bf16.
+// with the rows beside them, dw 4.1 TB/s mostly of stores); a single 2048 x
+// 2048 matrix with 32768 rows reaches 950 TFLOP/s in bf16.
 #include "grouped_device.h"
 
 namespace moe {

@@ -376,6 +376,45 @@ def test_long_reductions_of_few_rows(mb, K):
         check(out, y, m, gu.in_groups(off, 41), F32, k, 128, f"MXFP4 K={k}")
 
 
+@pytest.mark.parametrize("wide,odd", [(264, 257), (1096, 1090)])
+def test_as_many_tiles_as_compute_units(mb, wide, odd):
+    """Calls of up to one tile a compute unit, of 64 columns and of 128, with reductions of up to ten steps."""
+    _, E, off, rows = CASES["many rows"]
+    g = torch.Generator().manual_seed(wide)
+    used = gu.in_groups(off, rows)
+    for k in (72, 640):
+        for dtype, out_dtype in ((BF, BF), (HF, F32)):
+            say(f"one tile a unit {wide} k={k} {dtype}")
+            x, w = torch.randn(rows, k, generator=g).to(dtype), torch.randn(E, wide, k, generator=g).to(dtype)
+            out = torch.full((rows, wide), 7.0, dtype=out_dtype, device="cuda")
+            mb.grouped_gemm(strided(x, 8, float("nan")), dev(w), dev(off), out)
+            check(out, *gu.product(x.double(), w.double(), off, rows), used, out_dtype, k, 32, "fwd")
+            wt = w.transpose(1, 2).contiguous()  # [E][k][wide]
+            out.fill_(7.0)
+            mb.grouped_gemm_dx(strided(x, 8, float("nan")), dev(wt), dev(off), out)
+            check(out, *gu.product(x.double(), w.double(), off, rows), used, out_dtype, k, 32, "dx")
+        kx = 4 * k + 5
+        x, w = gu.mx_encode(torch.randn(rows, kx, generator=g)), gu.mx_encode(torch.randn(E * odd, kx, generator=g))
+        out = torch.full((rows, odd), 7.0, dtype=BF, device="cuda")
+        mb.mx_grouped_gemm((dev(x[0]), dev(x[1])), (dev(w[0]), dev(w[1])), E, kx, dev(off), out)
+        x64, w64 = gu.mx_decode(*x, kx), gu.mx_decode(*w, kx).reshape(E, odd, kx)
+        check(out, *gu.product(x64, w64, off, rows), used, BF, kx, 128, "MXFP4")
+        # SwiGLU of a product with itself: silu(p) p, half of the columns
+        half = odd // 2
+        part = [t.reshape(E, odd, -1)[:, :half].contiguous() for t in w]
+        out = torch.full((rows, half), 7.0, device="cuda")
+        m = (dev(part[0]), dev(part[1]))
+        mb.mx_grouped_gemm((dev(x[0]), dev(x[1])), m, E, kx, dev(off), out, up=m)
+        y, mag = gu.product(x64, w64[:, :half], off, rows)
+        err = gu.sum_bound(mag, kx, 128)
+        a = gu.silu(y)
+        # as in test_mx_grouped_gemm: |silu'| <= 1.1, both factors off by err
+        limit = 1.1 * err * (y.abs() + err) + (a.abs() + 1.1 * err) * err + 2.0 ** -20 * (a * y).abs()
+        got = out.cpu().double()
+        assert bool((got[~used] == 7.0).all())
+        assert bool(((got - a * y).abs()[used] <= gu.rounded(a * y, limit, F32)[used]).all())
+
+
 @pytest.mark.parametrize("op", ["gemm", "gemm_dx", "gemm_dw"])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF, F32), (HF, HF)])
 def test_many_tiles(mb, op, dtype, out_dtype):
